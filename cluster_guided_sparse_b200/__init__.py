@@ -262,3 +262,6 @@ def kmeans_noalloc(x: torch.Tensor, dim_off: int, dim_n: int, C: int, iters: int
                  ctypes.c_void_p(labels.data_ptr()), ctypes.c_void_p(centroids.data_ptr()),
                  _stream(stream, x.device)))
     return labels, centroids
+
+
+from .ops import rope, rope_backward  # noqa: E402  (the operators build on the names above)

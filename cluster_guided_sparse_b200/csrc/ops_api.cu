@@ -1,0 +1,234 @@
+// Host side of the operators around the sparse attention: argument checks,
+// workspace layout and launches.  Every argument check runs before any CUDA
+// call.
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <string>
+
+#include "../../include/scope.h"
+#include "op_common.cuh"
+
+scope_status scope_set_error(scope_status s, const char *msg);
+
+namespace scope {
+namespace op {
+bool check_tensor(const scope_tensor *t, const char *name, int64_t min_n, scope_status *st);
+RowStrides strides_of(const scope_tensor *t);
+}  // namespace op
+}  // namespace scope
+
+using namespace scope;
+
+namespace {
+
+scope_status fail(scope_status s, const char *fmt, ...)
+{
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return scope_set_error(s, buf);
+}
+
+bool same_shape(const scope_tensor *a, const scope_tensor *b)
+{
+    return a->B == b->B && a->H == b->H && a->N == b->N && a->D == b->D;
+}
+
+// Written in place: the very same rows.
+bool same_rows(const scope_tensor *a, const scope_tensor *b)
+{
+    const RowStrides x = op::strides_of(a), y = op::strides_of(b);
+    return (a->B == 1 || x.sB == y.sB) && (a->H == 1 || x.sH == y.sH) && (a->N == 1 || x.sN == y.sN);
+}
+
+scope_status check_over(const scope_tensor *out, const scope_tensor *in, const char *names)
+{
+    if (out->ptr == in->ptr && out->N > 0 && !same_rows(out, in))
+        return fail(SCOPE_EINVAL, "%s: same memory with other strides", names);
+    return SCOPE_OK;
+}
+
+bool float_type(int t) { return t == SCOPE_F32 || t == SCOPE_BF16 || t == SCOPE_F16; }
+
+[[maybe_unused]] size_t take(size_t &cur, size_t bytes)
+{
+    const size_t at = cur;
+    cur += (bytes + 255) & ~(size_t)255;
+    return at;
+}
+
+scope_status check_workspace(const void *ws, size_t have, size_t need)
+{
+    if (!ws) return fail(SCOPE_EWORKSPACE, "workspace: null");
+    if (((uintptr_t)ws) & 255) return fail(SCOPE_EALIGN, "workspace must be 256-byte aligned");
+    if (have < need) return fail(SCOPE_EWORKSPACE, "workspace too small: %zu < %zu bytes", have, need);
+    return SCOPE_OK;
+}
+
+// The current device is an sm_100 one.  (A stream of another device makes the
+// launch itself fail; asking for a stream's device would end a capture.)
+scope_status check_device()
+{
+    int dev = 0, major = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return fail(SCOPE_EDEVICE, "no CUDA device");
+    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    if (major != 10)
+        return fail(SCOPE_EDEVICE, "libscope.so is built for sm_100a; device has compute capability %d.x", major);
+    return SCOPE_OK;
+}
+
+scope_status launch_status(const char *what)
+{
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(SCOPE_ECUDA, "%s: %s", what, cudaGetErrorString(e));
+    return SCOPE_OK;
+}
+
+// ---------------------------------------------------------------- rotary positions
+scope_status check_rope(const scope_tensor *x, const scope_grid *g, const scope_params *p, const scope_positions *pos)
+{
+    if (!p) return fail(SCOPE_EINVAL, "params: null");
+    const int ds[3] = {p->d_t, p->d_h, p->d_w};
+    for (int s = 0; s < 3; ++s)
+        if (ds[s] < 0 || (ds[s] & 1)) return fail(SCOPE_ESHAPE, "params: d_t/d_h/d_w must be even and >= 0");
+    if ((int64_t)ds[0] + ds[1] + ds[2] != x->D) return fail(SCOPE_ESHAPE, "params: d_t + d_h + d_w must equal D");
+    if (!(p->theta > 0.0) || !std::isfinite(p->theta)) return fail(SCOPE_EINVAL, "params: theta must be finite and > 0");
+    const bool has_grid = g && (g->T || g->Hh || g->W);
+    if (pos) {
+        if (has_grid) return fail(SCOPE_EINVAL, "give a grid or positions, not both");
+        if (!pos->ptr && x->N) return fail(SCOPE_EINVAL, "positions: null data pointer");
+        if (((uintptr_t)pos->ptr) & 3) return fail(SCOPE_EALIGN, "positions: pointer not 4-byte aligned");
+        if (pos->B != 1 && pos->B != x->B) return fail(SCOPE_ESHAPE, "positions: B must be 1 or that of x");
+        return SCOPE_OK;
+    }
+    if (!has_grid) return fail(SCOPE_EINVAL, "give a grid or positions");
+    if (g->T < 1 || g->Hh < 1 || g->W < 1 || (int64_t)g->Hh * g->W > x->N || (int64_t)g->T * g->Hh * g->W != x->N)
+        return fail(SCOPE_ESHAPE, "grid: T*Hh*W must equal N");
+    return SCOPE_OK;
+}
+
+scope_status check_weight(const scope_vector *w, const char *name, float eps)
+{
+    if (!w->ptr) return fail(SCOPE_EINVAL, "%s: null data pointer", name);
+    if (!float_type(w->dtype)) return fail(SCOPE_EDTYPE, "%s: dtype must be f32, bf16 or f16", name);
+    if (((uintptr_t)w->ptr) & (w->dtype == SCOPE_F32 ? 3 : 1)) return fail(SCOPE_EALIGN, "%s: pointer not aligned", name);
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(SCOPE_EINVAL, "eps must be finite and >= 0");
+    return SCOPE_OK;
+}
+
+op::RopeTurns rope_turns(const scope_params *p)
+{
+    op::RopeTurns t{};
+    const int ds[3] = {p->d_t, p->d_h, p->d_w};
+    t.pt = p->d_t / 2;
+    t.ph = p->d_h / 2;
+    int at = 0;
+    for (int s = 0; s < 3; ++s)
+        for (int i = 0; i < ds[s] / 2; ++i)
+            t.turns[at++] = std::pow(p->theta, -2.0 * i / ds[s]) / (2.0 * M_PI);
+    return t;
+}
+
+op::RopeArgs rope_args(const scope_tensor *x, const scope_grid *g, const scope_positions *pos, const scope_vector *w,
+                       float eps, const scope_tensor *y)
+{
+    op::RopeArgs a{};
+    const RowStrides xs = op::strides_of(x), ys = op::strides_of(y);
+    a.x = x->ptr;
+    a.y = y->ptr;
+    a.xB = xs.sB; a.xH = xs.sH; a.xN = xs.sN;
+    a.yB = ys.sB; a.yH = ys.sH; a.yN = ys.sN;
+    a.Hh = 1;
+    a.W = 1;
+    if (pos) {
+        a.positions = pos->ptr;
+        a.posB = pos->B > 1 ? x->N * 3 : 0;
+    } else {
+        a.Hh = g->Hh;
+        a.W = g->W;
+    }
+    if (w) {
+        a.weight = w->ptr;
+        a.w_dtype = w->dtype;
+        a.eps = eps;
+    }
+    a.sign = 1.f;
+    a.H = (int)x->H;
+    a.N = (int)x->N;
+    a.D = (int)x->D;
+    a.tokens = x->B * x->N;
+    return a;
+}
+
+size_t rope_bwd_bytes(const scope_tensor *x)
+{
+    int hpb;
+    return 256 + (size_t)op::rope_bwd_blocks(x->B * x->N, (int)x->H, (int)x->D, &hpb) * x->D * 4;
+}
+
+}  // namespace
+
+extern "C" scope_status scope_rope(const scope_tensor *x, const scope_grid *grid, const scope_params *p,
+                                   const scope_positions *pos, const scope_vector *weight, float eps, int inverse,
+                                   scope_tensor *y, void *stream)
+{
+    scope_status st;
+    if (!op::check_tensor(x, "x", 0, &st) || !op::check_tensor(y, "y", 0, &st)) return st;
+    if (!same_shape(x, y)) return fail(SCOPE_ESHAPE, "x and y shapes differ");
+    if (x->dtype != y->dtype) return fail(SCOPE_EDTYPE, "x and y dtypes differ");
+    if ((st = check_over(y, x, "y, x")) != SCOPE_OK) return st;
+    if ((st = check_rope(x, grid, p, pos)) != SCOPE_OK) return st;
+    if (inverse != 0 && inverse != 1) return fail(SCOPE_EINVAL, "inverse must be 0 or 1");
+    if (weight) {
+        if ((st = check_weight(weight, "weight", eps)) != SCOPE_OK) return st;
+        if (inverse) return fail(SCOPE_EINVAL, "inverse does not go with a weight (see scope_rope_backward)");
+    }
+    if (x->N == 0) return SCOPE_OK;
+    if ((st = check_device()) != SCOPE_OK) return st;
+    op::RopeArgs a = rope_args(x, grid, pos, weight, eps, y);
+    if (inverse) a.sign = -1.f;
+    op::launch_rope_op(a, rope_turns(p), x->dtype, (cudaStream_t)stream);
+    return launch_status("scope_rope");
+}
+
+extern "C" size_t scope_rope_backward_workspace_bytes(const scope_tensor *x)
+{
+    scope_status st;
+    if (!op::check_tensor(x, "x", 0, &st)) return 0;
+    return rope_bwd_bytes(x);
+}
+
+extern "C" scope_status scope_rope_backward(const scope_tensor *dy, const scope_tensor *x, const scope_grid *grid,
+                                            const scope_params *p, const scope_positions *pos,
+                                            const scope_vector *weight, float eps, scope_tensor *dx, scope_vector *dw,
+                                            void *workspace, size_t ws_bytes, void *stream)
+{
+    scope_status st;
+    if (!op::check_tensor(dy, "dy", 0, &st) || !op::check_tensor(x, "x", 0, &st) || !op::check_tensor(dx, "dx", 0, &st))
+        return st;
+    if (!same_shape(x, dy) || !same_shape(x, dx)) return fail(SCOPE_ESHAPE, "x, dy and dx shapes differ");
+    if (x->dtype != dy->dtype || x->dtype != dx->dtype) return fail(SCOPE_EDTYPE, "x, dy and dx dtypes differ");
+    if ((st = check_over(dx, x, "dx, x")) != SCOPE_OK || (st = check_over(dx, dy, "dx, dy")) != SCOPE_OK) return st;
+    if ((st = check_rope(x, grid, p, pos)) != SCOPE_OK) return st;
+    if (!weight || !dw) return fail(SCOPE_EINVAL, "weight, dw: null (without a norm the gradient is scope_rope, inverse = 1)");
+    if ((st = check_weight(weight, "weight", eps)) != SCOPE_OK) return st;
+    if ((st = check_weight(dw, "dw", eps)) != SCOPE_OK) return st;
+    if (dw->dtype != weight->dtype) return fail(SCOPE_EDTYPE, "weight and dw dtypes differ");
+    if (dw->ptr == weight->ptr) return fail(SCOPE_EINVAL, "dw may not overlap weight");
+    if ((st = check_workspace(workspace, ws_bytes, rope_bwd_bytes(x))) != SCOPE_OK) return st;
+    if ((st = check_device()) != SCOPE_OK) return st;
+    if (x->N == 0) {
+        cudaMemsetAsync(dw->ptr, 0, (size_t)x->D * (dw->dtype == SCOPE_F32 ? 4 : 2), (cudaStream_t)stream);
+        return launch_status("scope_rope_backward");
+    }
+    op::RopeArgs a = rope_args(x, grid, pos, weight, eps, dx);
+    const RowStrides ds = op::strides_of(dy);
+    a.dy = dy->ptr;
+    a.dB = ds.sB; a.dH = ds.sH; a.dN = ds.sN;
+    a.dw_part = (float *)workspace;
+    op::launch_rope_op_bwd(a, rope_turns(p), x->dtype, dw->ptr, (cudaStream_t)stream);
+    return launch_status("scope_rope_backward");
+}

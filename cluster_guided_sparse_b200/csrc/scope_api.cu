@@ -64,6 +64,10 @@ void run_selection(const float *lut, const int32_t *codes, const int32_t *item_i
 size_t selection_state_bytes(int64_t clusters);
 size_t eg_state_bytes(int64_t B, int64_t H, int64_t Cq, int group);
 int block_count(int T, int Hh, int W, int kind, int bt, int bh, int bw);
+namespace op {
+bool check_tensor(const scope_tensor *t, const char *name, int64_t min_n, scope_status *st);
+RowStrides strides_of(const scope_tensor *t);
+}
 void launch_blocks(int T, int Hh, int W, int kind, int bt, int bh, int bw, const __nv_bfloat16 *kr, int32_t *codes,
                    float *cent, float *cn, int32_t *sizes, int BH, int N, int D, cudaStream_t st);
 }  // namespace scope
@@ -123,13 +127,15 @@ size_t take(size_t &cur, size_t bytes)
     return at;
 }
 
-bool tensor_ok(const scope_tensor *t, const char *name, scope_status *st)
+// f16, min_n: whether f16 is taken too, and the fewest rows (a tensor without
+// rows may have a null pointer).
+bool tensor_ok(const scope_tensor *t, const char *name, scope_status *st, bool f16 = false, int64_t min_n = 1)
 {
     if (!t) {
         *st = fail(SCOPE_EINVAL, "%s: null tensor", name);
         return false;
     }
-    if (!t->ptr) {
+    if (!t->ptr && (t->N != 0 || min_n > 0)) {
         *st = fail(SCOPE_EINVAL, "%s: null data pointer", name);
         return false;
     }
@@ -137,9 +143,9 @@ bool tensor_ok(const scope_tensor *t, const char *name, scope_status *st)
         *st = fail(SCOPE_EALIGN, "%s: pointer not 16-byte aligned", name);
         return false;
     }
-    if (t->B < 1 || t->H < 1 || t->N < 1) {
-        *st = fail(SCOPE_ESHAPE, "%s: B, H, N must be >= 1 (got %lld, %lld, %lld)", name, (long long)t->B,
-                   (long long)t->H, (long long)t->N);
+    if (t->B < 1 || t->H < 1 || t->N < min_n) {
+        *st = fail(SCOPE_ESHAPE, "%s: B, H must be >= 1 and N >= %d (got %lld, %lld, %lld)", name, (int)min_n,
+                   (long long)t->B, (long long)t->H, (long long)t->N);
         return false;
     }
     if (t->D != 64 && t->D != 128) {
@@ -154,8 +160,8 @@ bool tensor_ok(const scope_tensor *t, const char *name, scope_status *st)
         *st = fail(SCOPE_ESHAPE, "%s: N must be <= 2^24 (got %lld)", name, (long long)t->N);
         return false;
     }
-    if (t->dtype != SCOPE_F32 && t->dtype != SCOPE_BF16) {
-        *st = fail(SCOPE_EDTYPE, "%s: dtype must be f32 or bf16", name);
+    if (t->dtype != SCOPE_F32 && t->dtype != SCOPE_BF16 && !(f16 && t->dtype == SCOPE_F16)) {
+        *st = fail(SCOPE_EDTYPE, "%s: dtype must be f32%s bf16", name, f16 ? ", f16 or" : " or");
         return false;
     }
     const int64_t *sd = t->strides;
@@ -461,6 +467,13 @@ scope_status launch_status(const char *what)
 }
 
 }  // namespace
+
+bool scope::op::check_tensor(const scope_tensor *t, const char *name, int64_t min_n, scope_status *st)
+{
+    return tensor_ok(t, name, st, true, min_n);
+}
+
+scope::RowStrides scope::op::strides_of(const scope_tensor *t) { return rows_of(t); }
 
 struct scope_plan_s {
     Layout L;

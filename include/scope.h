@@ -49,14 +49,15 @@ typedef enum {
     SCOPE_F32 = 0,
     SCOPE_BF16 = 1,
     SCOPE_I32 = 2,
-    SCOPE_I64 = 3
+    SCOPE_I64 = 3,
+    SCOPE_F16 = 4 /* taken by the operators at the end of this file only */
 } scope_dtype;
 
 /* A caller-owned device tensor of logical shape [B, H, N, D].
  *   strides  element strides of the B, H, N and D dimensions.  strides[3]
  *            must be 1 (a row of D elements is contiguous); strides[0..2]
  *            must be >= 0 and keep every row start 16-byte aligned
- *            (multiples of 8 elements for bf16, of 4 for f32), and distinct
+ *            (multiples of 8 elements for bf16 and f16, of 4 for f32), and distinct
  *            (b, h, n) must not share a row.  All four zero means the
  *            contiguous layout {H*N*D, N*D, D, 1}.  Any other layout (for
  *            example [B, N, H, D] memory seen as [B, H, N, D], or every
@@ -308,6 +309,63 @@ size_t scope_kmeans_noalloc_scratch_bytes(int64_t B, int64_t H, int64_t N, int32
 scope_status scope_kmeans_noalloc(const scope_tensor *x, int32_t dim_off, int32_t dim_n,
                                   int32_t C, int32_t iters, uint32_t init_seed,
                                   int32_t *labels, float *centroids, void *stream);
+
+/* ---------------------------------------------------------------------- */
+/* Operators around the sparse attention of a transformer block.            */
+/*                                                                          */
+/* scope_rope (also behind a per-head RMS norm) makes the q and k of a      */
+/* scope_plan call without grid, of scope_cross_attn, or of any attention   */
+/* whose tokens do not fill one raster grid.  scope_cross_attn attends to   */
+/* states of another length; with k, v of the queries' own sequence it is   */
+/* dense self-attention with gradients.  The conventions above hold, and    */
+/*   - f16 is taken next to bf16 (and f32 by the rotations);                */
+/*   - a tensor without rows (N = 0) is taken; its pointer may be null;     */
+/*   - an output may not overlap an input or another output, except that   */
+/*     scope_rope may write y over x and scope_rope_backward dx over x or  */
+/*     dy (the very same rows).                                             */
+/*   - equal calls give equal bits: no sum depends on the order of atomics. */
+/*   - a bounded wait that runs out is reported by scope_ops_sync_status.   */
+/* ---------------------------------------------------------------------- */
+
+/* Positions of the tokens on the (t, h, w) axes: int32 [B][N][3], device,
+ * any values (negative ones too); B = 1: shared by the whole batch. */
+typedef struct {
+    const int32_t *ptr;
+    int64_t B;
+} scope_positions;
+
+/* A vector of D numbers (f32, bf16 or f16), device. */
+typedef struct {
+    void *ptr;
+    scope_dtype dtype;
+} scope_vector;
+
+/* Rotary positions: pair i of axis block s (p->d_t, d_h, d_w; interleaved
+ * pairs (2i, 2i+1), as scope_plan) turns by pos_s * theta^(-2i/d_s), for each
+ * of the heads alike.
+ *   x, y       [B,H,N,D] f32, bf16 or f16, same shape and dtype; N >= 0.
+ *   grid, pos  exactly one: a raster grid (T*Hh*W == N), or positions (grid
+ *              NULL or {0,0,0}).
+ *   weight     NULL, or the weight of an RMS norm over each row that comes
+ *              before the rotation: z = x * (mean(x^2) + eps)^-1/2 * weight.
+ *   eps        >= 0 (with a weight only).
+ *   inverse    1: turns by the negative angles (the gradient of the plain
+ *              rotation); not with a weight.
+ * Only d_t, d_h, d_w and theta of `p` are read.  Angles are reduced in 64
+ * bits; the norm and the rotation run in 32, rounded once. */
+scope_status scope_rope(const scope_tensor *x, const scope_grid *grid, const scope_params *p,
+                        const scope_positions *pos, const scope_vector *weight, float eps, int inverse,
+                        scope_tensor *y, void *stream);
+
+/* Gradients of scope_rope with a weight (without one: scope_rope of dy with
+ * inverse = 1): dx from dy and the call's x, and dw [D] (weight's dtype), the
+ * sum over all rows.
+ *   workspace  >= scope_rope_backward_workspace_bytes(x) bytes, 256-B aligned. */
+size_t scope_rope_backward_workspace_bytes(const scope_tensor *x);
+scope_status scope_rope_backward(const scope_tensor *dy, const scope_tensor *x, const scope_grid *grid,
+                                 const scope_params *p, const scope_positions *pos, const scope_vector *weight,
+                                 float eps, scope_tensor *dx, scope_vector *dw, void *workspace, size_t ws_bytes,
+                                 void *stream);
 
 /* Number of kernels this library has launched in this process so far (all
  * devices, all threads); a diagnostic for launch accounting. */

@@ -1,0 +1,136 @@
+"""Host-only checks of the operators around the sparse attention: every refusal
+comes from the argument checks, which run before any CUDA call (the pointers
+are fake), and the 64-bit forms that the GPU tests use agree with their own
+differences."""
+import ctypes
+
+import pytest
+import torch
+
+import cluster_guided_sparse_b200 as scope
+import op_ref as R
+from cluster_guided_sparse_b200 import build, ops
+
+FAKE = 0x7F0000000000  # aligned, never dereferenced
+EINVAL, ESHAPE, EDTYPE, EALIGN, EWORKSPACE = 1, 2, 3, 4, 5
+by = ctypes.byref
+
+
+@pytest.fixture(scope="module")
+def L():
+    build.build()
+    return ops._functions()
+
+
+def T(B=1, H=2, N=256, D=64, dtype=scope.SCOPE_BF16, ptr=FAKE, strides=None):
+    return scope.ScopeTensor(ptr, dtype, B, H, N, D, (ctypes.c_int64 * 4)(*(strides or (0, 0, 0, 0))))
+
+
+def prm(**kw):
+    return scope.make_params(**{**dict(d_t=16, d_h=24, d_w=24, theta=10000.0), **kw})[0]
+
+
+def rope_status(L, x=None, y=None, grid=(4, 8, 8), p=None, pos=None, w=None, eps=1e-6, inverse=0):
+    g = scope.ScopeGrid(*grid)
+    st = L.scope_rope(by(x or T()), by(g), by(p or prm()), pos and by(pos), w and by(w), eps, inverse,
+                      by(y or T(ptr=FAKE + 4096)), None)
+    return st, L.scope_last_error().decode()
+
+
+@pytest.mark.parametrize("kw,code,msg", [
+    (dict(p=prm(d_t=15, d_h=25)), ESHAPE, "even"),
+    (dict(p=prm(d_t=16, d_h=24, d_w=26)), ESHAPE, "equal D"),
+    (dict(p=prm(theta=0.0)), EINVAL, "theta"),
+    (dict(p=prm(theta=float("inf"))), EINVAL, "theta"),
+    (dict(p=prm(theta=float("nan"))), EINVAL, "theta"),
+    (dict(grid=(4, 8, 7)), ESHAPE, "grid"),
+    (dict(grid=(4, 0, 64)), ESHAPE, "grid"),
+    (dict(grid=(-4, -8, 8)), ESHAPE, "grid"),
+    (dict(grid=(1, 65536, 65537)), ESHAPE, "grid"),  # the product passes 32 bits
+    (dict(grid=(0, 0, 0)), EINVAL, "grid or positions"),
+    (dict(pos=ops.ScopePositions(FAKE, 1)), EINVAL, "not both"),
+    (dict(grid=(0, 0, 0), pos=ops.ScopePositions(0, 1)), EINVAL, "null"),
+    (dict(grid=(0, 0, 0), pos=ops.ScopePositions(FAKE + 2, 1)), EALIGN, "4-byte"),
+    (dict(grid=(0, 0, 0), pos=ops.ScopePositions(FAKE, 3)), ESHAPE, "positions"),
+    (dict(w=ops.ScopeVector(0, 0)), EINVAL, "null"),
+    (dict(w=ops.ScopeVector(FAKE, 2)), EDTYPE, "weight"),
+    (dict(w=ops.ScopeVector(FAKE + 2, 0)), EALIGN, "weight"),
+    (dict(w=ops.ScopeVector(FAKE, 0), eps=-1.0), EINVAL, "eps"),
+    (dict(w=ops.ScopeVector(FAKE, 0), eps=float("nan")), EINVAL, "eps"),
+    (dict(w=ops.ScopeVector(FAKE, 0), inverse=1), EINVAL, "inverse"),
+    (dict(inverse=2), EINVAL, "inverse"),
+    (dict(x=T(ptr=0)), EINVAL, "null"),
+    (dict(x=T(ptr=FAKE + 8)), EALIGN, "aligned"),
+    (dict(x=T(D=96)), ESHAPE, "head dim"),
+    (dict(x=T(dtype=scope.SCOPE_I32)), EDTYPE, "dtype"),
+    (dict(x=T(strides=(0, 64, 0, 1))), ESHAPE, "overlap"),
+    (dict(x=T(strides=(0, 64 * 256, 68, 1))), ESHAPE, "16 bytes"),
+    (dict(x=T(strides=(0, 64 * 256, 128, 2))), ESHAPE, "strides[3]"),
+    (dict(y=T(N=255)), ESHAPE, "differ"),
+    (dict(y=T(dtype=scope.SCOPE_F32)), EDTYPE, "differ"),
+    (dict(y=T(strides=(0, 64, 128, 1))), EINVAL, "same memory"),
+])
+def test_rope_refusals(L, kw, code, msg):
+    st, err = rope_status(L, **kw)
+    assert st == code and msg in err, (st, err)
+
+
+def test_rope_without_rows_needs_no_device(L):
+    x = T(N=0, ptr=0, dtype=ops.SCOPE_F16)
+    assert rope_status(L, x=x, y=x, grid=(0, 0, 0), pos=ops.ScopePositions(0, 1))[0] == 0
+
+
+def rope_backward_status(L, w, dw, ws=FAKE, ws_bytes=1 << 30, dx=None):
+    x, g = T(), scope.ScopeGrid(4, 8, 8)
+    st = L.scope_rope_backward(by(T()), by(x), by(g), by(prm()), None, w and by(w), 1e-6, by(dx or T()),
+                               dw and by(dw), ws, ws_bytes, None)
+    return st, L.scope_last_error().decode()
+
+
+@pytest.mark.parametrize("kw,code,msg", [
+    (dict(w=None, dw=None), EINVAL, "inverse"),
+    (dict(w=ops.ScopeVector(FAKE, 0), dw=None), EINVAL, "dw"),
+    (dict(w=ops.ScopeVector(FAKE, 0), dw=ops.ScopeVector(FAKE + 512, 1)), EDTYPE, "differ"),
+    (dict(w=ops.ScopeVector(FAKE, 0), dw=ops.ScopeVector(FAKE, 0)), EINVAL, "overlap"),
+    (dict(w=ops.ScopeVector(FAKE, 0), dw=ops.ScopeVector(FAKE + 512, 0), ws=None), EWORKSPACE, "null"),
+    (dict(w=ops.ScopeVector(FAKE, 0), dw=ops.ScopeVector(FAKE + 512, 0), ws=FAKE + 16), EALIGN, "256"),
+    (dict(w=ops.ScopeVector(FAKE, 0), dw=ops.ScopeVector(FAKE + 512, 0), ws_bytes=64), EWORKSPACE, "small"),
+    (dict(w=ops.ScopeVector(FAKE, 0), dw=ops.ScopeVector(FAKE + 512, 0), dx=T(H=3)), ESHAPE, "differ"),
+    (dict(w=ops.ScopeVector(FAKE, 0), dw=ops.ScopeVector(FAKE + 512, 0), dx=T(strides=(0, 64, 128, 1))), EINVAL,
+     "same memory"),
+])
+def test_rope_backward_refusals(L, kw, code, msg):
+    st, err = rope_backward_status(L, **kw)
+    assert st == code and msg in err, (st, err)
+
+
+def test_bindings_refuse_cpu_tensors_and_wrong_shapes():
+    x = torch.zeros(1, 2, 256, 64)
+    with pytest.raises(ValueError, match="CUDA"):
+        scope.rope(x, prm(), scope.ScopeGrid(4, 8, 8))
+    with pytest.raises(ValueError, match="B, H, N, D"):
+        ops._tensor(x[0], "x")
+    with pytest.raises(ValueError, match="dtype"):
+        ops._tensor(x.double(), "x")
+    with pytest.raises(ValueError, match="int32"):
+        ops._positions(torch.zeros(256, 3, dtype=torch.int64), x)
+    with pytest.raises(ValueError, match="positions must be"):
+        ops._positions(torch.zeros(2, 256, 3, dtype=torch.int32), x)
+    with pytest.raises(ValueError, match="vector"):
+        ops._vector(torch.zeros(65), 64, "weight")
+    with pytest.raises(ValueError, match="vector"):
+        ops._vector(torch.zeros(128)[::2], 64, "weight")
+
+
+def test_rope_formula_gradients_agree_with_differences():
+    g = torch.Generator().manual_seed(0)
+    x, dy = (torch.randn(2, 3, 5, 64, generator=g, dtype=torch.float64) for _ in range(2))
+    w = 1 + 0.3 * torch.randn(64, generator=g, dtype=torch.float64)
+    pos = torch.randint(-50, 50, (2, 5, 3), generator=g, dtype=torch.int32)
+    a = R.angles((16, 24, 24), 1e4, 5, positions=pos)
+    dx, dw = R.rope_grads(dy, x, a, w, 1e-6)
+    u, v = torch.randn(x.shape, generator=g, dtype=torch.float64), torch.randn(64, generator=g, dtype=torch.float64)
+    f = lambda s: (R.turn(R.norm(x + s * u, w + s * v, 1e-6), a) * dy).sum()  # noqa: E731
+    h = 1e-5  # truncation h^2 of O(1) third derivatives, cancellation 1e-16 * 1e3 / h
+    want = (f(h) - f(-h)) / (2 * h)
+    assert abs((dx * u).sum() + (dw * v).sum() - want) < 1e-6
