@@ -1,13 +1,14 @@
 // Host side of the operators around the sparse attention: argument checks,
 // workspace layout and launches.  Every argument check runs before any CUDA
 // call.
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <string>
 
 #include "../../include/scope.h"
-#include "op_common.cuh"
+#include "cross_common.cuh"
 
 scope_status scope_set_error(scope_status s, const char *msg);
 
@@ -53,7 +54,7 @@ scope_status check_over(const scope_tensor *out, const scope_tensor *in, const c
 
 bool float_type(int t) { return t == SCOPE_F32 || t == SCOPE_BF16 || t == SCOPE_F16; }
 
-[[maybe_unused]] size_t take(size_t &cur, size_t bytes)
+size_t take(size_t &cur, size_t bytes)
 {
     const size_t at = cur;
     cur += (bytes + 255) & ~(size_t)255;
@@ -231,4 +232,180 @@ extern "C" scope_status scope_rope_backward(const scope_tensor *dy, const scope_
     a.dw_part = (float *)workspace;
     op::launch_rope_op_bwd(a, rope_turns(p), x->dtype, dw->ptr, (cudaStream_t)stream);
     return launch_status("scope_rope_backward");
+}
+
+// ---------------------------------------------------------------- cross attention
+namespace {
+
+constexpr int kSms = 148;  // of a B200; work is split for this many whatever part of one is visible
+
+scope_status check_keys(const scope_tensor *k, const scope_keys *keys)
+{
+    if (!keys) return SCOPE_OK;
+    if (keys->len && keys->mask) return fail(SCOPE_EINVAL, "keys: give a length or a mask, not both");
+    if (((uintptr_t)keys->len) & 3) return fail(SCOPE_EALIGN, "keys: len not 4-byte aligned");
+    if (keys->mask && keys->mask_stride < 0)
+        return fail(SCOPE_ESHAPE, "keys: mask_stride must be >= 0");
+    return SCOPE_OK;
+}
+
+scope_status check_qk(const scope_tensor *q, const scope_tensor *k)
+{
+    scope_status st;
+    if (!op::check_tensor(q, "q", 0, &st) || !op::check_tensor(k, "k", 0, &st)) return st;
+    if (q->dtype == SCOPE_F32) return fail(SCOPE_EDTYPE, "q: dtype must be bf16 or f16");
+    if (q->dtype != k->dtype) return fail(SCOPE_EDTYPE, "q and k dtypes differ");
+    if (q->D != k->D) return fail(SCOPE_ESHAPE, "q and k head dims differ");
+    if (k->B != q->B && k->B != 1) return fail(SCOPE_ESHAPE, "k: B must be 1 or that of q");
+    if (q->H % k->H) return fail(SCOPE_ESHAPE, "the key heads must divide the query heads");
+    if (q->B * q->H * q->N > ((int64_t)1 << 30)) return fail(SCOPE_ESHAPE, "q: B*H*N must be <= 2^30");
+    return SCOPE_OK;
+}
+
+scope_status check_cross(const scope_tensor *q, const scope_tensor *k, const scope_tensor *v, const scope_keys *keys,
+                         float scale)
+{
+    scope_status st;
+    if ((st = check_qk(q, k)) != SCOPE_OK) return st;
+    if (!op::check_tensor(v, "v", 0, &st)) return st;
+    if (!same_shape(k, v)) return fail(SCOPE_ESHAPE, "k and v shapes differ");
+    if (v->dtype != k->dtype) return fail(SCOPE_EDTYPE, "k and v dtypes differ");
+    if ((st = check_keys(k, keys)) != SCOPE_OK) return st;
+    if (scale != 0.f && !(scale >= 1e-30f && scale <= 1e30f))
+        return fail(SCOPE_EINVAL, "scale must be 0 (1/sqrt(D)) or in [1e-30, 1e30]");
+    return SCOPE_OK;
+}
+
+// `t` has the shape and dtype of `like`.
+scope_status check_as(const scope_tensor *t, const char *name, const scope_tensor *like, const char *like_name)
+{
+    scope_status st;
+    if (!op::check_tensor(t, name, 0, &st)) return st;
+    if (!same_shape(t, like)) return fail(SCOPE_ESHAPE, "%s and %s shapes differ", name, like_name);
+    if (t->dtype != like->dtype) return fail(SCOPE_EDTYPE, "%s and %s dtypes differ", name, like_name);
+    return SCOPE_OK;
+}
+
+// No two of an output and any other tensor start at one address.
+scope_status check_apart(const scope_tensor *const *t, int n, int outputs)
+{
+    for (int i = 0; i < outputs; ++i)
+        for (int j = i + 1; j < n; ++j)
+            if (t[i]->ptr && t[i]->ptr == t[j]->ptr)
+                return fail(SCOPE_EINVAL, "an output may not overlap another tensor");
+    return SCOPE_OK;
+}
+
+scope_status cross_ready()
+{
+    const scope_status st = check_device();
+    if (st != SCOPE_OK) return st;
+    static std::atomic<bool> configured[64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 64 && configured[dev]) return SCOPE_OK;
+    if (op::cross_fwd_configure() != cudaSuccess) return fail(SCOPE_ECUDA, "kernel attribute setup failed");
+    if (dev < 64) configured[dev] = true;
+    return SCOPE_OK;
+}
+
+// Offsets into the workspace.
+struct CrossLayout {
+    size_t idx, cnt, part_o, part_lse, total;
+};
+
+op::CrossArgs cross_sizes(const scope_tensor *q, const scope_tensor *k)
+{
+    op::CrossArgs a{};
+    a.B = (int)q->B; a.Bk = (int)k->B; a.H = (int)q->H; a.Hk = (int)k->H; a.N = (int)q->N; a.M = (int)k->N;
+    a.G = a.H / a.Hk;
+    a.GN = a.G * a.N;
+    a.rows = a.Bk == a.B ? a.GN : a.B * a.GN;
+    a.sets = a.Bk * a.Hk;
+    a.row_tiles = (a.rows + 255) / 256;
+    return a;
+}
+
+CrossLayout cross_layout(op::CrossArgs &a, int D, bool masked)
+{
+    CrossLayout L{};
+    const int64_t total = (int64_t)a.B * a.H * a.N;
+    a.splits = op::cross_fwd_splits(a.sets, a.row_tiles, a.M, total, D, kSms);
+    a.items = a.sets * a.splits * a.row_tiles;
+    size_t cur = 256;
+    L.idx = take(cur, masked ? (size_t)a.Bk * a.M * 4 : 0);
+    L.cnt = take(cur, masked ? (size_t)a.Bk * 4 : 0);
+    L.part_o = take(cur, a.splits > 1 ? (size_t)a.splits * total * D * 4 : 0);
+    L.part_lse = take(cur, a.splits > 1 ? (size_t)a.splits * total * 4 : 0);
+    L.total = cur;
+    return L;
+}
+
+void cross_tensors(op::CrossArgs &a, const scope_tensor *q, const scope_tensor *k, const scope_tensor *v,
+                   const scope_tensor *o, const scope_keys *keys, float scale)
+{
+    const RowStrides qs = op::strides_of(q), ks = op::strides_of(k), vs = op::strides_of(v), os = op::strides_of(o);
+    a.q = q->ptr; a.k = k->ptr; a.v = v->ptr; a.o = o->ptr;
+    a.qB = qs.sB; a.qH = qs.sH; a.qN = qs.sN;
+    a.kB = ks.sB; a.kH = ks.sH; a.kN = ks.sN;
+    a.vB = vs.sB; a.vH = vs.sH; a.vN = vs.sN;
+    a.oB = os.sB; a.oH = os.sH; a.oN = os.sN;
+    a.kv_len = keys ? keys->len : nullptr;
+    a.scale = scale != 0.f ? scale : 1.f / std::sqrt((float)q->D);
+    a.scale_log2 = a.scale * 1.4426950408889634f;
+}
+
+}  // namespace
+
+extern "C" size_t scope_cross_attn_workspace_bytes(const scope_tensor *q, const scope_tensor *k, int masked)
+{
+    if (check_qk(q, k) != SCOPE_OK) return 0;
+    op::CrossArgs a = cross_sizes(q, k);
+    return cross_layout(a, (int)q->D, masked != 0).total;
+}
+
+extern "C" scope_status scope_cross_attn(const scope_tensor *q, const scope_tensor *k, const scope_tensor *v,
+                                         const scope_keys *keys, float scale, scope_tensor *o, float *lse,
+                                         void *workspace, size_t ws_bytes, void *stream)
+{
+    scope_status st;
+    if ((st = check_cross(q, k, v, keys, scale)) != SCOPE_OK) return st;
+    if ((st = check_as(o, "o", q, "q")) != SCOPE_OK) return st;
+    const scope_tensor *all[4] = {o, q, k, v};
+    if ((st = check_apart(all, 4, 1)) != SCOPE_OK) return st;
+    if (((uintptr_t)lse) & 3) return fail(SCOPE_EALIGN, "lse: pointer not 4-byte aligned");
+    op::CrossArgs a = cross_sizes(q, k);
+    const bool masked = keys && keys->mask;
+    const CrossLayout L = cross_layout(a, (int)q->D, masked);
+    if ((st = check_workspace(workspace, ws_bytes, L.total)) != SCOPE_OK) return st;
+    if (q->N == 0) return SCOPE_OK;
+    if ((st = cross_ready()) != SCOPE_OK) return st;
+    cross_tensors(a, q, k, v, o, keys, scale);
+    a.lse = lse;
+    char *ws = (char *)workspace;
+    a.part_o = (float *)(ws + L.part_o);
+    a.part_lse = (float *)(ws + L.part_lse);
+    cudaStream_t s = (cudaStream_t)stream;
+    if (masked) {
+        int32_t *idx = (int32_t *)(ws + L.idx), *cnt = (int32_t *)(ws + L.cnt);
+        op::launch_key_lists(keys->mask, keys->mask_stride, a.Bk, a.M, idx, cnt, nullptr, s);
+        a.idx = idx;
+        a.cnt = cnt;
+    }
+    op::launch_cross_fwd(a, (int)q->D, q->dtype == SCOPE_F16, kSms, s);
+    return launch_status("scope_cross_attn");
+}
+
+extern "C" scope_status scope_ops_sync_status(void *stream)
+{
+    const scope_status st = check_device();
+    if (st != SCOPE_OK) return st;
+    cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
+    if (e != cudaSuccess) return fail(SCOPE_ECUDA, "stream: %s", cudaGetErrorString(e));
+    int32_t err[4] = {0, 0, 0, 0};
+    e = op::cross_fwd_error(err, true);
+    if (e != cudaSuccess) return fail(SCOPE_ECUDA, "reading the error word: %s", cudaGetErrorString(e));
+    if (err[0] & kErrTimeout) return fail(SCOPE_ETIMEOUT, "a bounded device wait gave up (detail 0x%x)", err[1]);
+    if (err[0]) return fail(SCOPE_EDEVICE, "device range check fired (flags 0x%x, detail 0x%x)", err[0], err[1]);
+    return SCOPE_OK;
 }

@@ -1,5 +1,6 @@
 """Operators around the sparse attention of a transformer block: rotary
-positions, the same behind a per-head RMS norm, with gradients.
+positions, the same behind a per-head RMS norm, and cross attention to states
+of another length, with gradients.
 
 Argument marshalling over libscope.so, as in the package's other entry points:
 tensors are [B, H, N, D] device tensors of any layout with contiguous, 16-byte
@@ -32,6 +33,10 @@ class ScopeVector(ctypes.Structure):
     _fields_ = [("ptr", ctypes.c_void_p), ("dtype", ctypes.c_int)]
 
 
+class ScopeKeys(ctypes.Structure):
+    _fields_ = [("len", ctypes.c_void_p), ("mask", ctypes.c_void_p), ("mask_stride", ctypes.c_int64)]
+
+
 @functools.lru_cache(maxsize=None)
 def _functions():
     """libscope.so with these operators' argument types set."""
@@ -41,6 +46,10 @@ def _functions():
     L.scope_rope_backward_workspace_bytes.argtypes = [T]
     L.scope_rope_backward_workspace_bytes.restype = Z
     L.scope_rope_backward.argtypes = [T, T, G, R, P(ScopePositions), P(ScopeVector), F, T, P(ScopeVector), V, Z, V]
+    L.scope_cross_attn_workspace_bytes.argtypes = [T, T, ctypes.c_int]
+    L.scope_cross_attn_workspace_bytes.restype = Z
+    L.scope_cross_attn.argtypes = [T, T, T, P(ScopeKeys), F, T, V, V, Z, V]
+    L.scope_ops_sync_status.argtypes = [V]
     return L
 
 
@@ -172,3 +181,68 @@ def rope_backward(dy: torch.Tensor, x: torch.Tensor, params: ScopeParams, grid: 
          pos, ctypes.byref(w), eps, ctypes.byref(_tensor(dx, "out")), ctypes.byref(_vector(dw, x.shape[-1], "dw")),
          ws.data_ptr(), ws.numel() * ws.element_size())
     return dx, dw
+
+
+def _keys(k: torch.Tensor, kv_len: Optional[torch.Tensor], kv_mask: Optional[torch.Tensor]):
+    Bk, M = k.shape[0], k.shape[2]
+    if kv_len is not None and (kv_len.dtype != torch.int32 or tuple(kv_len.shape) != (Bk,) or not kv_len.is_contiguous()):
+        raise ValueError(f"kv_len must be contiguous int32 [{Bk}]")
+    if kv_mask is None:
+        return None if kv_len is None else ctypes.byref(ScopeKeys(kv_len.data_ptr(), None, 0))
+    if kv_mask.dtype not in (torch.bool, torch.uint8) or tuple(kv_mask.shape) != (Bk, M) or (M > 1 and kv_mask.stride(1) != 1):
+        raise ValueError(f"kv_mask must be bool or uint8 [{Bk}, {M}] with contiguous rows")
+    # a mask without keys has no memory: as a length of zero, any address serves
+    return ctypes.byref(ScopeKeys(None if kv_len is None else kv_len.data_ptr(), kv_mask.data_ptr() if M else None,
+                                  kv_mask.stride(0)))
+
+
+@functools.lru_cache(maxsize=4096)
+def _cross_bytes(name: str, q_shape, k_shape, dtype: torch.dtype, masked: bool) -> int:
+    """Workspace of a call with these shapes."""
+    L, dt = _functions(), _DT[dtype]
+    fake = 1 << 20  # sizes do not depend on addresses or strides
+    q, k = (ScopeTensor(fake, dt, *s, _I4(0, 0, 0, 0)) for s in (q_shape, k_shape))
+    need = getattr(L, name)(ctypes.byref(q), ctypes.byref(k), int(masked))
+    if need == 0:
+        raise ScopeError(1, L.scope_last_error().decode())
+    return need
+
+
+def cross_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, kv_len: Optional[torch.Tensor] = None,
+               kv_mask: Optional[torch.Tensor] = None, scale: Optional[float] = None, return_lse: bool = False,
+               out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """softmax(scale q k^T) v of q [B, H, N, D] over k, v [Bk, Hk, M, D] (bf16 or
+    f16): Bk is B, or 1 for states shared by the batch; Hk divides H.  Keys
+    from kv_len (int32 [Bk]) on, or where kv_mask (bool [Bk, M]) is False, are
+    not read.  scale: 1/sqrt(D).  return_lse: (o, lse) with lse f32 [B, H, N],
+    which cross_attn_backward takes."""
+    dev = _device(q, k, v, kv_len, kv_mask, out, workspace)
+    call = _Launch(dev, stream, q, k, v, kv_len, kv_mask, out, workspace)
+    tq, tk, tv = _tensor(q, "q"), _tensor(k, "k"), _tensor(v, "v")
+    keys = _keys(k, kv_len, kv_mask)
+    ws = call.workspace(workspace, _cross_bytes("scope_cross_attn_workspace_bytes", q.shape, k.shape, q.dtype,
+                                                kv_mask is not None))
+    o = call.like(q, out)
+    lse = call.empty(q.shape[:3], torch.float32) if return_lse else None
+    call(_functions().scope_cross_attn, ctypes.byref(tq), ctypes.byref(tk), ctypes.byref(tv), keys,
+         _scale(scale), ctypes.byref(_tensor(o, "out")), lse.data_ptr() if return_lse else None, ws.data_ptr(),
+         ws.numel() * ws.element_size())
+    return (o, lse) if return_lse else o
+
+
+def _scale(scale: Optional[float]) -> float:
+    if scale is None:
+        return 0.0
+    if not 1e-30 <= scale <= 1e30:
+        raise ValueError(f"scale must be in [1e-30, 1e30] (got {scale})")
+    return scale
+
+
+def ops_sync_status(stream=None, device=None):
+    """Synchronises the stream (by default the device's current one) and raises
+    ScopeError if a bounded wait of the package's operators gave up since the
+    last report."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    with torch.cuda.device(stream.device):
+        _check(_functions().scope_ops_sync_status(stream.cuda_stream))

@@ -367,6 +367,44 @@ scope_status scope_rope_backward(const scope_tensor *dy, const scope_tensor *x, 
                                  float eps, scope_tensor *dx, scope_vector *dw, void *workspace, size_t ws_bytes,
                                  void *stream);
 
+/* Which keys a row may read: at most one of len and mask; neither (or a NULL
+ * scope_keys): all M.  Keys a row may not read are never loaded, so they may
+ * hold anything (infinities, NaN); a row that may read none gets o = 0,
+ * lse = -inf and zero gradients.
+ *   len   int32 [Bk], device: keys [0, len) (values are held to [0, M]).
+ *   mask  bytes [Bk][M], device, rows mask_stride >= 0 bytes apart (0: one
+ *         row for the whole batch): non-zero = may be read. */
+typedef struct {
+    const int32_t *len;
+    const uint8_t *mask;
+    int64_t mask_stride;
+} scope_keys;
+
+/* Cross attention: o_i = sum_j softmax_j(scale q_i . k_j) v_j over the keys j
+ * that row i may read, M keys for N queries.
+ *   q, o   [B,H,N,D] bf16 or f16; N >= 0.
+ *   k, v   [Bk,Hk,M,D], q's dtype; M >= 0.  Bk is B, or 1: one set of states
+ *          shared by the batch.  Hk divides H: query heads [g H/Hk, (g+1) H/Hk)
+ *          read key head g.
+ *   scale  0: 1/sqrt(D); else in [1e-30, 1e30].
+ *   lse    NULL, or f32 [B][H][N], device: ln sum_j exp(scale q_i . k_j); the
+ *          backward pass needs it.
+ *   workspace  >= scope_cross_attn_workspace_bytes bytes, 256-B aligned
+ *          (masked: whether a mask is given).
+ * B*H*N <= 2^30.  Scores, softmax statistics and sums are held in 32 bits;
+ * softmax weights (and in the backward pass ds) are rounded to the inputs' type as
+ * operands of the tensor cores. */
+size_t scope_cross_attn_workspace_bytes(const scope_tensor *q, const scope_tensor *k, int masked);
+scope_status scope_cross_attn(const scope_tensor *q, const scope_tensor *k, const scope_tensor *v,
+                              const scope_keys *keys, float scale, scope_tensor *o, float *lse, void *workspace,
+                              size_t ws_bytes, void *stream);
+
+/* Synchronises `stream` and reports the error word that the operators share on
+ * the current device, then clears it: SCOPE_OK, SCOPE_ETIMEOUT (a bounded wait
+ * gave up: outputs of calls since the last report may be wrong), SCOPE_EDEVICE
+ * or SCOPE_ECUDA.  Not during a stream capture. */
+scope_status scope_ops_sync_status(void *stream);
+
 /* Number of kernels this library has launched in this process so far (all
  * devices, all threads); a diagnostic for launch accounting. */
 int64_t scope_kernel_launches(void);

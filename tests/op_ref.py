@@ -93,3 +93,90 @@ def within(got, want, bound, what):
     err = (got.double() - want).abs()
     bad = ~(err <= bound)
     assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()} off, worst {float((err - bound).max()):.3e} above the bound"
+
+
+# ---------------------------------------------------------------- cross attention
+def allowed_keys(Bk, M, kv_len=None, kv_mask=None, device="cpu"):
+    if kv_mask is not None:
+        return kv_mask.bool()
+    if kv_len is not None:
+        return torch.arange(M, device=device)[None] < kv_len[:, None]
+    return torch.ones((Bk, M), dtype=torch.bool, device=device)
+
+
+def cross(q, k, v, allowed, scale, dtype, do=None):
+    """Values and bounds of o, lse (and with do: dq, dk, dv) in 64 bits.
+
+    es: scores are fp32 sums of D exact products; a sum of n terms is off by at
+    most n 2^-23 of the sum of absolute values (adders that cut off: one whole
+    step a term).  ep, relative to p: es; 2^-22 of the largest score (scale
+    times log2 e, and the row's lse, are each rounded); the fused scale and
+    shift, and the exponential's 2 ulp, 2^-18 where p > 2^-64.  For the
+    normalised p once more the same, for the sum.
+    P is rounded to `dtype`: h of itself, or f (half the least subnormal)
+    against a row maximum of 1; products with P sum 16 exact products a step.
+    """
+    B, H, N, D = q.shape
+    Bk, Hk, M, _ = k.shape
+    G, fi = H // Hk, torch.finfo(dtype)
+    h, f = fi.eps / 2, fi.smallest_normal * fi.eps / 2
+    dev = q.device
+    z = lambda *s: torch.zeros(s, dtype=torch.float64, device=dev)  # noqa: E731
+    r = dict(o=z(B, H, N, D), lse=torch.full((B, H, N), -torch.inf, dtype=torch.float64, device=dev))
+    b = dict(o=z(B, H, N, D), lse=z(B, H, N))
+    if do is not None:
+        for t in (r, b):
+            t.update(dq=z(B, H, N, D), dk=z(Bk, Hk, M, D), dv=z(Bk, Hk, M, D))
+    q, k, v = q.double(), k.double(), v.double()
+    do = None if do is None else do.double()
+    for bi in range(B):
+        kb = bi if Bk == B else 0
+        on = allowed[kb].nonzero()[:, 0]
+        if len(on) == 0:
+            continue
+        for hi in range(H):
+            hk = hi // G
+            Q, K, V = q[bi, hi], k[kb, hk][on], v[kb, hk][on]
+            s = scale * Q @ K.T
+            es = D * 2.0 ** -23 * scale * (Q.abs() @ K.abs().T)
+            ep = es + s.abs().amax(-1, keepdim=True) * 2.0 ** -22 + 2.0 ** -18
+            lse = torch.logsumexp(s, -1, keepdim=True)
+            p = torch.exp(s - lse)
+            epn = ep + (p * ep).sum(-1, keepdim=True)
+            o = p @ V
+            acc = (len(on) / 16 + 16) * 2.0 ** -23
+            bo = (p * (h + epn + acc) + f) @ V.abs()
+            r["o"][bi, hi], b["o"][bi, hi] = o, bo
+            r["lse"][bi, hi] = lse[:, 0]
+            b["lse"][bi, hi] = (p * ep).sum(-1) + acc + 2.0 ** -21 * (1 + lse[:, 0].abs())
+            if do is None:
+                continue
+            dO = do[bi, hi]
+            dp = dO @ V.T
+            Dl = (dO * o).sum(-1, keepdim=True)
+            ds = p * (dp - Dl)
+            edp = D * 2.0 ** -23 * (dO.abs() @ V.abs().T)
+            eD = (dO.abs() * (bo + half_ulp(o, dtype) + o.abs() * D * 2.0 ** -23)).sum(-1, keepdim=True)
+            pb = b["lse"][bi, hi][:, None] + ep  # p from the stored lse
+            bds = ds.abs() * (h + pb + 2.0 ** -22) + p * (edp + eD) * (1 + pb) + f
+            rows = ((B * G if Bk < B else G) * N / 16 + 16) * 2.0 ** -23
+            r["dq"][bi, hi] = scale * ds @ K
+            b["dq"][bi, hi] = scale * ((bds + ds.abs() * acc) @ K.abs())
+            r["dk"][kb, hk].index_add_(0, on, scale * ds.T @ Q)
+            b["dk"][kb, hk].index_add_(0, on, scale * (bds + ds.abs() * rows).T @ Q.abs())
+            r["dv"][kb, hk].index_add_(0, on, p.T @ dO)
+            b["dv"][kb, hk].index_add_(0, on, (p * (h + pb + rows) + f).T @ dO.abs())
+    for n in r:
+        if n != "lse":
+            b[n] = b[n] + half_ulp(r[n], dtype)
+    return r, b
+
+
+def check_cross(got, r, b, names):
+    for n in names:
+        if n == "lse":
+            none = torch.isinf(r[n])
+            assert (got[n][none] == -torch.inf).all(), "lse of rows without keys"
+            within(got[n][~none], r[n][~none], b[n][~none], n)
+        else:
+            within(got[n], r[n], b[n], n)

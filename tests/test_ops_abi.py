@@ -134,3 +134,94 @@ def test_rope_formula_gradients_agree_with_differences():
     h = 1e-5  # truncation h^2 of O(1) third derivatives, cancellation 1e-16 * 1e3 / h
     want = (f(h) - f(-h)) / (2 * h)
     assert abs((dx * u).sum() + (dw * v).sum() - want) < 1e-6
+
+
+def cross_status(L, q=None, k=None, v=None, keys=None, scale=0.0, o=None, ws=FAKE, ws_bytes=1 << 40, lse=None):
+    k = k or T(N=77, ptr=FAKE + (1 << 20))
+    q = q or T()
+    o = o or T(q.B, q.H, q.N, q.D, q.dtype, FAKE + (3 << 20))
+    v = v or T(k.B, k.H, k.N, k.D, k.dtype, FAKE + (2 << 20))
+    st = L.scope_cross_attn(by(q), by(k), by(v), keys and by(keys), scale, by(o), lse, ws, ws_bytes, None)
+    return st, L.scope_last_error().decode()
+
+
+CROSS_REFUSALS = [
+    (dict(q=T(dtype=scope.SCOPE_F32)), EDTYPE, "bf16 or f16"),
+    (dict(k=T(N=77, dtype=ops.SCOPE_F16)), EDTYPE, "differ"),
+    (dict(k=T(N=77, D=128)), ESHAPE, "head dims"),
+    (dict(q=T(B=4), k=T(B=2, N=77)), ESHAPE, "B must be 1"),
+    (dict(q=T(H=6), k=T(H=4, N=77)), ESHAPE, "divide"),
+    (dict(q=T(H=2), k=T(H=4, N=77)), ESHAPE, "divide"),
+    (dict(q=T(B=64, H=3, N=1 << 23), k=T(B=64, H=1, N=77)), ESHAPE, "2^30"),
+    (dict(v=T(N=76)), ESHAPE, "differ"),
+    (dict(v=T(N=77, dtype=ops.SCOPE_F16)), EDTYPE, "differ"),
+    (dict(k=T(N=77, strides=(0, 0, 64, 1))), ESHAPE, "overlap"),
+    (dict(k=T(N=77, ptr=0)), EINVAL, "null"),
+    (dict(keys=ops.ScopeKeys(FAKE, FAKE, 77)), EINVAL, "not both"),
+    (dict(keys=ops.ScopeKeys(FAKE + 1, None, 0)), EALIGN, "len"),
+    (dict(keys=ops.ScopeKeys(None, FAKE, -1)), ESHAPE, "mask_stride"),
+    (dict(scale=-1.0), EINVAL, "scale"),
+    (dict(scale=float("nan")), EINVAL, "scale"),
+    (dict(scale=float("inf")), EINVAL, "scale"),
+    (dict(scale=1e-38), EINVAL, "scale"),
+    (dict(o=T(N=255)), ESHAPE, "differ"),
+    (dict(o=T(dtype=ops.SCOPE_F16)), EDTYPE, "differ"),
+    (dict(o=T()), EINVAL, "overlap"),
+    (dict(lse=FAKE + 2), EALIGN, "lse"),
+    (dict(ws=None), EWORKSPACE, "null"),
+    (dict(ws=FAKE + 16), EALIGN, "256"),
+    (dict(ws_bytes=0), EWORKSPACE, "small"),
+]
+
+
+@pytest.mark.parametrize("kw,code,msg", CROSS_REFUSALS)
+def test_cross_attn_refusals(L, kw, code, msg):
+    st, err = cross_status(L, **kw)
+    assert st == code and msg in err, (st, err)
+
+
+def test_cross_attn_workspace(L):
+    size = lambda q, k, m=0: L.scope_cross_attn_workspace_bytes(by(q), by(k), m)  # noqa: E731
+    assert size(T(H=24, N=118800, D=128), T(H=24, N=256, D=128)) == 256  # rows enough: keys are not split
+    k = T(B=2, N=1000)
+    assert size(T(B=2, N=118800), k, 1) >= size(T(B=2, N=118800), k) + 2 * 1000 * 4
+    one = size(T(H=1, N=1), T(H=1, N=118800))  # a single row: ranges of keys with fp32 outputs
+    assert one > 256 + 100 * 64 * 4
+    assert size(T(dtype=scope.SCOPE_F32), T(dtype=scope.SCOPE_F32)) == 0
+
+
+def test_cross_bindings_refuse_wrong_masks():
+    k = torch.zeros(2, 3, 77, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="kv_len"):
+        ops._keys(k, torch.zeros(2, dtype=torch.int64), None)
+    with pytest.raises(ValueError, match="kv_len"):
+        ops._keys(k, torch.zeros(3, dtype=torch.int32), None)
+    with pytest.raises(ValueError, match="kv_mask"):
+        ops._keys(k, None, torch.zeros(2, 76, dtype=torch.bool))
+    with pytest.raises(ValueError, match="kv_mask"):
+        ops._keys(k, None, torch.zeros(2, 77))
+    with pytest.raises(ValueError, match="kv_mask"):
+        ops._keys(k, None, torch.zeros(77, 2, dtype=torch.bool).T)
+    with pytest.raises(ValueError, match="scale"):
+        ops._scale(0.0)
+    with pytest.raises(ValueError, match="CUDA"):
+        scope.cross_attn(k, k, k)
+
+
+def test_cross_formula_gradients_agree_with_differences():
+    g = torch.Generator().manual_seed(1)
+    q = torch.randn(2, 4, 5, 64, generator=g, dtype=torch.float64)
+    k, v = (torch.randn(1, 2, 7, 64, generator=g, dtype=torch.float64) for _ in range(2))
+    do = torch.randn(q.shape, generator=g, dtype=torch.float64)
+    on = torch.tensor([[1, 0, 1, 1, 0, 1, 1]], dtype=torch.bool)
+    r, _ = R.cross(q, k, v, on, 0.125, torch.bfloat16, do)
+    dirs = [torch.randn(t.shape, generator=g, dtype=torch.float64) for t in (q, k, v)]
+
+    def f(s):
+        return (R.cross(q + s * dirs[0], k + s * dirs[1], v + s * dirs[2], on, 0.125, torch.bfloat16)[0]["o"] * do).sum()
+
+    h = 1e-5  # h^2 times third derivatives of order 1e2, and cancellation
+    want = (f(h) - f(-h)) / (2 * h)
+    got = sum((r[n] * d).sum() for n, d in zip(("dq", "dk", "dv"), dirs))
+    assert abs(got - want) < 1e-6
+    assert (r["dk"][0, :, ~on[0]] == 0).all() and (r["dv"][0, :, ~on[0]] == 0).all()
