@@ -304,7 +304,8 @@ scope_status cross_ready()
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 64 && configured[dev]) return SCOPE_OK;
-    if (op::cross_fwd_configure() != cudaSuccess) return fail(SCOPE_ECUDA, "kernel attribute setup failed");
+    if (op::cross_fwd_configure() != cudaSuccess || op::cross_bwd_configure() != cudaSuccess)
+        return fail(SCOPE_ECUDA, "kernel attribute setup failed");
     if (dev < 64) configured[dev] = true;
     return SCOPE_OK;
 }
@@ -337,6 +338,32 @@ CrossLayout cross_layout(op::CrossArgs &a, int D, bool masked)
     L.cnt = take(cur, masked ? (size_t)a.Bk * 4 : 0);
     L.part_o = take(cur, a.splits > 1 ? (size_t)a.splits * total * D * 4 : 0);
     L.part_lse = take(cur, a.splits > 1 ? (size_t)a.splits * total * 4 : 0);
+    L.total = cur;
+    return L;
+}
+
+struct CrossBwdLayout {
+    size_t idx, cnt, inv, nlse, ndelta, part_dq, part_dk, part_dv, total;
+};
+
+CrossBwdLayout cross_bwd_layout(op::CrossArgs &a, int D, bool masked)
+{
+    CrossBwdLayout L{};
+    const int64_t total = (int64_t)a.B * a.H * a.N;
+    a.rows_pad = (a.rows + 127) / 128 * 128;
+    a.dq_splits = op::cross_dq_splits(a.sets, a.rows, a.M, total, D, kSms);
+    a.dkv_splits = op::cross_dkv_splits(a.sets, a.rows, a.M, D, kSms);
+    size_t cur = 256;
+    const size_t keys = masked ? (size_t)a.Bk * a.M * 4 : 0, rows = (size_t)a.sets * a.rows_pad * 4;
+    L.idx = take(cur, keys);
+    L.inv = take(cur, keys);
+    L.cnt = take(cur, masked ? (size_t)a.Bk * 4 : 0);
+    L.nlse = take(cur, rows);
+    L.ndelta = take(cur, rows);
+    L.part_dq = take(cur, a.dq_splits > 1 ? (size_t)a.dq_splits * total * D * 4 : 0);
+    const size_t parts = (size_t)a.dkv_splits * a.sets * a.M * D * 4;
+    L.part_dk = take(cur, parts);
+    L.part_dv = take(cur, parts);
     L.total = cur;
     return L;
 }
@@ -396,6 +423,62 @@ extern "C" scope_status scope_cross_attn(const scope_tensor *q, const scope_tens
     return launch_status("scope_cross_attn");
 }
 
+extern "C" size_t scope_cross_attn_backward_workspace_bytes(const scope_tensor *q, const scope_tensor *k, int masked)
+{
+    if (check_qk(q, k) != SCOPE_OK) return 0;
+    op::CrossArgs a = cross_sizes(q, k);
+    return cross_bwd_layout(a, (int)q->D, masked != 0).total;
+}
+
+extern "C" scope_status scope_cross_attn_backward(const scope_tensor *d_o, const scope_tensor *q, const scope_tensor *k,
+                                                  const scope_tensor *v, const scope_tensor *o, const float *lse,
+                                                  const scope_keys *keys, float scale, scope_tensor *dq,
+                                                  scope_tensor *dk, scope_tensor *dv, void *workspace, size_t ws_bytes,
+                                                  void *stream)
+{
+    scope_status st;
+    if ((st = check_cross(q, k, v, keys, scale)) != SCOPE_OK) return st;
+    if ((st = check_as(d_o, "d_o", q, "q")) != SCOPE_OK || (st = check_as(o, "o", q, "q")) != SCOPE_OK ||
+        (st = check_as(dq, "dq", q, "q")) != SCOPE_OK || (st = check_as(dk, "dk", k, "k")) != SCOPE_OK ||
+        (st = check_as(dv, "dv", k, "k")) != SCOPE_OK)
+        return st;
+    const scope_tensor *all[8] = {dq, dk, dv, d_o, q, k, v, o};
+    if ((st = check_apart(all, 8, 3)) != SCOPE_OK) return st;
+    if (!lse && q->N) return fail(SCOPE_EINVAL, "lse: null data pointer");
+    if (((uintptr_t)lse) & 3) return fail(SCOPE_EALIGN, "lse: pointer not 4-byte aligned");
+    op::CrossArgs a = cross_sizes(q, k);
+    const bool masked = keys && keys->mask;
+    const CrossBwdLayout L = cross_bwd_layout(a, (int)q->D, masked);
+    if ((st = check_workspace(workspace, ws_bytes, L.total)) != SCOPE_OK) return st;
+    if (q->N == 0 && k->N == 0) return SCOPE_OK;
+    if ((st = cross_ready()) != SCOPE_OK) return st;
+    cross_tensors(a, q, k, v, o, keys, scale);
+    const RowStrides ds = op::strides_of(d_o), qs = op::strides_of(dq), ks = op::strides_of(dk), vs = op::strides_of(dv);
+    a.dout = d_o->ptr;
+    a.dB = ds.sB; a.dH = ds.sH; a.dN = ds.sN;
+    a.dq = dq->ptr;
+    a.dqB = qs.sB; a.dqH = qs.sH; a.dqN = qs.sN;
+    a.lse = const_cast<float *>(lse);  // read only here
+    char *ws = (char *)workspace;
+    a.nlse = (float *)(ws + L.nlse);
+    a.ndelta = (float *)(ws + L.ndelta);
+    a.part_dq = (float *)(ws + L.part_dq);
+    a.part_dk = (float *)(ws + L.part_dk);
+    a.part_dv = (float *)(ws + L.part_dv);
+    cudaStream_t s = (cudaStream_t)stream;
+    int32_t *inv = nullptr;
+    if (masked) {
+        int32_t *idx = (int32_t *)(ws + L.idx), *cnt = (int32_t *)(ws + L.cnt);
+        inv = (int32_t *)(ws + L.inv);
+        op::launch_key_lists(keys->mask, keys->mask_stride, a.Bk, a.M, idx, cnt, inv, s);
+        a.idx = idx;
+        a.cnt = cnt;
+    }
+    const int64_t dks[3] = {ks.sB, ks.sH, ks.sN}, dvs[3] = {vs.sB, vs.sH, vs.sN};
+    op::launch_cross_bwd(a, (int)q->D, q->dtype == SCOPE_F16, kSms, inv, dk->ptr, dks, dv->ptr, dvs, s);
+    return launch_status("scope_cross_attn_backward");
+}
+
 extern "C" scope_status scope_ops_sync_status(void *stream)
 {
     const scope_status st = check_device();
@@ -404,6 +487,10 @@ extern "C" scope_status scope_ops_sync_status(void *stream)
     if (e != cudaSuccess) return fail(SCOPE_ECUDA, "stream: %s", cudaGetErrorString(e));
     int32_t err[4] = {0, 0, 0, 0};
     e = op::cross_fwd_error(err, true);
+    int32_t bwd[4] = {0, 0, 0, 0};
+    if (e == cudaSuccess) e = op::cross_bwd_error(bwd, true);
+    if (!err[1]) err[1] = bwd[1];
+    err[0] |= bwd[0];
     if (e != cudaSuccess) return fail(SCOPE_ECUDA, "reading the error word: %s", cudaGetErrorString(e));
     if (err[0] & kErrTimeout) return fail(SCOPE_ETIMEOUT, "a bounded device wait gave up (detail 0x%x)", err[1]);
     if (err[0]) return fail(SCOPE_EDEVICE, "device range check fired (flags 0x%x, detail 0x%x)", err[0], err[1]);

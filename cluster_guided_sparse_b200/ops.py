@@ -49,6 +49,9 @@ def _functions():
     L.scope_cross_attn_workspace_bytes.argtypes = [T, T, ctypes.c_int]
     L.scope_cross_attn_workspace_bytes.restype = Z
     L.scope_cross_attn.argtypes = [T, T, T, P(ScopeKeys), F, T, V, V, Z, V]
+    L.scope_cross_attn_backward_workspace_bytes.argtypes = [T, T, ctypes.c_int]
+    L.scope_cross_attn_backward_workspace_bytes.restype = Z
+    L.scope_cross_attn_backward.argtypes = [T, T, T, T, T, V, P(ScopeKeys), F, T, T, T, V, Z, V]
     L.scope_ops_sync_status.argtypes = [V]
     return L
 
@@ -228,6 +231,31 @@ def cross_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, kv_len: Opt
          _scale(scale), ctypes.byref(_tensor(o, "out")), lse.data_ptr() if return_lse else None, ws.data_ptr(),
          ws.numel() * ws.element_size())
     return (o, lse) if return_lse else o
+
+
+def cross_attn_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
+                        lse: torch.Tensor, *, kv_len: Optional[torch.Tensor] = None,
+                        kv_mask: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                        dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
+                        dv: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """(dq, dk, dv) of cross_attn(q, k, v, ...) for the gradient `do` of its
+    output, from its results o and lse (return_lse=True) and the same masks and
+    scale.  dk and dv have k's shape: summed over the query heads that read a
+    key head and, for states shared by the batch, over the batch."""
+    dev = _device(q, do, k, v, o, lse, kv_len, kv_mask, dq, dk, dv, workspace)
+    call = _Launch(dev, stream, do, q, k, v, o, lse, kv_len, kv_mask, dq, dk, dv, workspace)
+    tdo, tq, tk, tv, to = (_tensor(t, n) for t, n in ((do, "do"), (q, "q"), (k, "k"), (v, "v"), (o, "o")))
+    if lse.dtype != torch.float32 or lse.shape != q.shape[:3] or not lse.is_contiguous():
+        raise ValueError(f"lse must be contiguous float32 {list(q.shape[:3])}")
+    keys = _keys(k, kv_len, kv_mask)
+    ws = call.workspace(workspace, _cross_bytes("scope_cross_attn_backward_workspace_bytes", q.shape, k.shape, q.dtype,
+                                                kv_mask is not None))
+    dq, dk, dv = call.like(q, dq), call.like(k, dk), call.like(v, dv)
+    ref = ctypes.byref
+    call(_functions().scope_cross_attn_backward, ref(tdo), ref(tq), ref(tk), ref(tv), ref(to), lse.data_ptr(), keys,
+         _scale(scale), ref(_tensor(dq, "dq")), ref(_tensor(dk, "dk")), ref(_tensor(dv, "dv")), ws.data_ptr(),
+         ws.numel() * ws.element_size())
+    return dq, dk, dv
 
 
 def _scale(scale: Optional[float]) -> float:

@@ -399,6 +399,20 @@ scope_status scope_cross_attn(const scope_tensor *q, const scope_tensor *k, cons
                               const scope_keys *keys, float scale, scope_tensor *o, float *lse, void *workspace,
                               size_t ws_bytes, void *stream);
 
+/* Gradients of scope_cross_attn for the gradient d_o of its output, from the
+ * call's q, k, v, keys and scale and its results o and lse.
+ *   d_o, dq    [B,H,N,D], q's dtype.
+ *   dk, dv     [Bk,Hk,M,D], q's dtype, written in full: summed over the query
+ *              heads of a key head and, for Bk = 1, over the batch; zero for keys
+ *              that no row may read.
+ *   workspace  >= scope_cross_attn_backward_workspace_bytes bytes, 256-B aligned.
+ * With f16, ds = p (dp - d_o . o) is held in f16: scale the loss as usual. */
+size_t scope_cross_attn_backward_workspace_bytes(const scope_tensor *q, const scope_tensor *k, int masked);
+scope_status scope_cross_attn_backward(const scope_tensor *d_o, const scope_tensor *q, const scope_tensor *k,
+                                       const scope_tensor *v, const scope_tensor *o, const float *lse,
+                                       const scope_keys *keys, float scale, scope_tensor *dq, scope_tensor *dk,
+                                       scope_tensor *dv, void *workspace, size_t ws_bytes, void *stream);
+
 /* Synchronises `stream` and reports the error word that the operators share on
  * the current device, then clears it: SCOPE_OK, SCOPE_ETIMEOUT (a bounded wait
  * gave up: outputs of calls since the last report may be wrong), SCOPE_EDEVICE

@@ -225,3 +225,44 @@ def test_cross_formula_gradients_agree_with_differences():
     got = sum((r[n] * d).sum() for n, d in zip(("dq", "dk", "dv"), dirs))
     assert abs(got - want) < 1e-6
     assert (r["dk"][0, :, ~on[0]] == 0).all() and (r["dv"][0, :, ~on[0]] == 0).all()
+
+
+def cross_backward_status(L, **over):
+    at = iter(range(FAKE, FAKE + (64 << 20), 1 << 20))
+    t = {n: T(N=256, ptr=next(at)) for n in ("d_o", "q", "o", "dq")}
+    t.update({n: T(N=77, ptr=next(at)) for n in ("k", "v", "dk", "dv")})
+    rest = dict(lse=FAKE, keys=None, scale=0.0, ws=FAKE, ws_bytes=1 << 40)
+    for n, x in over.items():
+        (t if n in t else rest)[n] = x
+    keys = rest["keys"]
+    st = L.scope_cross_attn_backward(by(t["d_o"]), by(t["q"]), by(t["k"]), by(t["v"]), by(t["o"]), rest["lse"],
+                                     keys and by(keys), rest["scale"], by(t["dq"]), by(t["dk"]), by(t["dv"]),
+                                     rest["ws"], rest["ws_bytes"], None)
+    return st, L.scope_last_error().decode()
+
+
+@pytest.mark.parametrize("kw,code,msg", [
+    (dict(d_o=T(N=255)), ESHAPE, "d_o and q"),
+    (dict(o=T(dtype=ops.SCOPE_F16)), EDTYPE, "o and q"),
+    (dict(dq=T(H=4)), ESHAPE, "dq and q"),
+    (dict(dk=T(N=76)), ESHAPE, "dk and k"),
+    (dict(dv=T(N=77, dtype=ops.SCOPE_F16)), EDTYPE, "dv and k"),
+    (dict(dv=T(N=77, strides=(0, 0, 64, 1))), ESHAPE, "overlap"),
+    (dict(dk=T(N=77, ptr=FAKE), dv=T(N=77, ptr=FAKE)), EINVAL, "overlap"),
+    (dict(dq=T(ptr=FAKE)), EINVAL, "overlap"),
+    (dict(lse=None), EINVAL, "lse"),
+    (dict(lse=FAKE + 1), EALIGN, "lse"),
+    (dict(scale=-1.0), EINVAL, "scale"),
+    (dict(keys=ops.ScopeKeys(FAKE, FAKE, 77)), EINVAL, "not both"),
+    (dict(ws=None), EWORKSPACE, "null"),
+    (dict(ws=FAKE + 128), EALIGN, "256"),
+    (dict(ws_bytes=256), EWORKSPACE, "small"),
+])
+def test_cross_attn_backward_refusals(L, kw, code, msg):
+    st, err = cross_backward_status(L, **kw)
+    assert st == code and msg in err, (st, err)
+
+
+def test_cross_attn_backward_without_rows_and_keys_needs_no_device(L):
+    none = {n: T(N=0, ptr=0) for n in ("d_o", "q", "o", "dq", "k", "v", "dk", "dv")}
+    assert cross_backward_status(L, lse=None, **none)[0] == 0
