@@ -18,11 +18,10 @@
 // products.
 //
 // Warp roles (384 threads):
-//   warps 0-3, 4-7  softmax and epilogue of tile 0, 1 (one thread per row)
-//   warp 8          Q rows     } coalesced 16-byte cp.async into 128B-swizzled
-//   warps 9-10      K, V rows  } tiles; any stride, key list or length works
-//                                alike, and rows past the end are zero-filled,
-//                                so masked keys are never read
+//   warps 0-3, 4-7  softmax and epilogue of tile 0, 1 (one thread per row); O
+//                   leaves through the item's Q buffer as whole row segments
+//   warp 8          Q rows     } by TMA, or cp.async where a tile's rows are not
+//   warps 9-10      K, V rows  } in order (cross_common.cuh)
 //   warp 11         tcgen05.mma issuer (one lane), owns the TMEM allocation
 // TMEM (512 columns): S0 [0,128) S1 [128,256) O0 [256,256+D) O1 [384,384+D);
 // P (16 bit) overwrites its S.  The softmax runs in base 2 with a lazy
@@ -54,19 +53,19 @@ constexpr int fwd_stages(int D) { return D == 128 ? 3 : 4; }
 constexpr size_t fwd_smem(int D) { return (size_t)(4 + fwd_stages(D)) * kTile * D * 2 + 1024; }
 
 struct FwdItem {
-    int bk, hk, r0, nq, t0, t1, nk, split;
+    int bk, hk, t0, t1, nk, split;
+    RowTile r;
 };
 
 __device__ __forceinline__ FwdItem fwd_item(const CrossArgs &a, int item)
 {
     FwdItem w;
-    const int rt = item % a.row_tiles, rest = item / a.row_tiles;
+    const int rt = item % a.pairs, rest = item / a.pairs;
     w.split = rest % a.splits;
     const int set = rest / a.splits;
     w.bk = set / a.Hk;
     w.hk = set % a.Hk;
-    w.r0 = rt * 2 * kTile;
-    w.nq = min(2 * kTile, a.rows - w.r0);
+    w.r = row_tile<2 * kTile>(a, w.bk, w.hk, rt);
     w.nk = keys_of(a, w.bk);
     const int tiles = (w.nk + kTile - 1) / kTile;
     w.t0 = (int)((int64_t)tiles * w.split / a.splits);
@@ -75,7 +74,7 @@ __device__ __forceinline__ FwdItem fwd_item(const CrossArgs &a, int item)
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_constant__ CrossArgs a)
+__global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_constant__ CrossArgs a, const __grid_constant__ CrossMaps m)
 {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = (unsigned char *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -92,7 +91,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
-            mbar_init(&q_empty[i], 1);
+            mbar_init(&q_empty[i], 8);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
             mbar_init(&o_full[i], 1);
@@ -118,26 +117,22 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_
     if (warp == 8) {
         // ------------------------------------------------------------ Q rows
         int qi = 0;
+        bool ok = true;
         for (int item = blockIdx.x; item < a.items; item += gridDim.x) {
             const FwdItem w = fwd_item(a, item);
             if (w.t0 == w.t1) continue;
             const int buf = qi & 1;
-            if (qi >= 2 && !wait.warp(&q_empty[buf], ((qi >> 1) - 1) & 1, 0x40)) break;
-            const int fill = w.nq > kTile ? 2 * kTile : kTile;
-            copy_rows<T, D>(a, w.bk, w.hk, w.r0, w.nq, fill, static_cast<const T *>(a.q), a.qB, a.qH, a.qN,
-                            smem_u32(sQ + buf * 2 * TB), lane, 32);
-            cp_async_commit();
-            cp_async_wait_all();
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&q_full[buf]);
+            if (qi >= 2 && !(ok = wait.warp(&q_empty[buf], ((qi >> 1) - 1) & 1, 0x40))) break;
+            load_rows<T, D>(a, w.r, w.hk, w.r.nq > kTile ? 2 : 1, &m.q, a.q, a.qB, a.qH, a.qN,
+                            smem_u32(sQ + buf * 2 * TB), &q_full[buf]);
             ++qi;
         }
+        if (!ok)
+            for (int i = qi - 2; i < qi; ++i) drain(&q_full[i & 1], (i >> 1) & 1);
     } else if (warp == 9 || warp == 10) {
         // ------------------------------------------------------------ K, V rows
         const int tid = threadIdx.x - 9 * 32;
         RingFill<NS> ring(kv_full, kv_empty);
-        KeyTile<T, D, 64> tile;
         bool ok = true;
         for (int item = blockIdx.x; ok && item < a.items; item += gridDim.x) {
             const FwdItem w = fwd_item(a, item);
@@ -145,16 +140,21 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_
             const T *v = static_cast<const T *>(a.v) + w.bk * a.vB + w.hk * a.vH;
             const int32_t *list = a.idx ? a.idx + (int64_t)w.bk * a.M : nullptr;
             for (int j = w.t0; ok && j < w.t1; ++j) {
-                tile.load(list, w.nk, j, tid);
-                if (!(ok = ring.acquire(wait, 0x41))) break;
-                tile.copy(k, a.kN, smem_u32(sKV + ring.slot * TB), tid);
-                ring.issued();
-                if (!(ok = ring.acquire(wait, 0x41))) break;
-                tile.copy(v, a.vN, smem_u32(sKV + ring.slot * TB), tid);
-                ring.issued();
+                const bool whole = tma_keys(a, w.nk, j);
+#pragma unroll 1
+                for (int x = 0; x < 2; ++x) {
+                    if (!(ok = ring.acquire(wait, 0x41))) break;
+                    const uint32_t dst = smem_u32(sKV + ring.slot * TB);
+                    if (whole) {
+                        ring.template tma<D>(warp == 9, dst, x ? &m.v : &m.k, j * kTile, w.hk, w.bk);
+                    } else {
+                        copy_keys<T, D, 64>(list, w.nk, j, x ? v : k, x ? a.vN : a.kN, dst, tid);
+                        ring.issued();
+                    }
+                }
             }
         }
-        ring.flush();
+        ring.finish(!ok);
     } else if (warp == 11) {
         // ------------------------------------------------------------ MMA issuer
         if (lane == 0) {
@@ -168,9 +168,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_
             for (int item = blockIdx.x; ok && item < a.items; item += gridDim.x) {
                 const FwdItem w = fwd_item(a, item);
                 if (w.t0 == w.t1) continue;
-                const int nt = w.nq > kTile ? 2 : 1, buf = qi & 1;
+                const int nt = w.r.nq > kTile ? 2 : 1, buf = qi & 1;
                 // S_t = Q_t K^T
-                auto issue_qk = [&](int t, int ks, bool last) {
+                auto issue_qk = [&](int t, int ks) {
                     const uint64_t aq = dq + (uint64_t)(((buf * 2 + t) * TB) >> 4);
                     const uint64_t bk = dk + (uint64_t)((ks * TB) >> 4);
 #pragma unroll
@@ -179,15 +179,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_
                         mma_ss(tmem + t * 128, aq + o, bk + o, id_qk, k > 0);
                     }
                     mma_commit(&s_full[t]);
-                    if (t == nt - 1) {
-                        mma_commit(&kv_empty[ks]);
-                        if (last) mma_commit(&q_empty[buf]);
-                    }
+                    if (t == nt - 1) mma_commit(&kv_empty[ks]);
                 };
                 ok = wait(&q_full[buf], (qi >> 1) & 1, 0x42) && wait(&kv_full[kv.slot], kv.use & 1, 0x43);
                 if (!ok) break;
                 tc_fence_after();
-                for (int t = 0; t < nt; ++t) issue_qk(t, kv.slot, w.t0 + 1 == w.t1);
+                for (int t = 0; t < nt; ++t) issue_qk(t, kv.slot);
                 kv.next();
                 for (int j = w.t0; ok && j < w.t1; ++j) {
                     const int vs = kv.slot;
@@ -209,7 +206,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_
                         if (more) {
                             if (t == 0 && !(ok = wait(&kv_full[kv.slot], kv.use & 1, 0x47))) break;
                             tc_fence_after();
-                            issue_qk(t, kv.slot, j + 2 == w.t1);
+                            issue_qk(t, kv.slot);
                         } else {
                             mma_commit(&o_full[t]);
                             ++no[t];
@@ -226,11 +223,21 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_
         const int t = warp >> 2, wq = warp & 3, row = wq * 32 + lane;
         const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
         const uint32_t tS = tmem + lane_off + t * 128, tO = tmem + lane_off + 256 + t * 128;
-        int ns = 0, no = 0;
+        int ns = 0, no = 0, qi = 0;
         bool ok = true;
         for (int item = blockIdx.x; ok && item < a.items; item += gridDim.x) {
             const FwdItem w = fwd_item(a, item);
-            if (w.nq <= t * kTile) continue;
+            const bool some = w.t0 < w.t1;  // uniform for the CTA
+            const int buf = qi & 1;
+            if (some) ++qi;
+            if (w.r.nq <= t * kTile) {
+                // no rows here: the item's Q is free as far as this tile goes (but not before it has come)
+                if (some) {
+                    if (!(ok = wait.warp(&q_full[buf], ((qi - 1) >> 1) & 1, 0x4c))) break;
+                    if (lane == 0) mbar_arrive(&q_empty[buf]);
+                }
+                continue;
+            }
             float m_run = -INFINITY, l = 0.f;
             for (int j = w.t0; j < w.t1; ++j) {
                 if (!(ok = wait.warp(&s_full[t], ns & 1, 0x48 + t))) break;
@@ -305,48 +312,68 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_
                 if (lane == 0) mbar_arrive(&p_full[t]);
             }
             if (!ok) break;
-            const bool some = w.t0 < w.t1;  // uniform for the CTA
             if (some) {
                 if (!(ok = wait.warp(&o_full[t], no & 1, 0x4a + t))) break;
                 ++no;
                 tc_fence_after();
             }
-            const int ri = t * kTile + row;
-            const bool store = ri < w.nq;
+            // all products of the item are done: the O rows leave through this tile's part of the Q buffer
+            const uint32_t stage = smem_u32(sQ + (buf * 2 + t) * TB) + wq * (TB / 4);
+            const int first = t * kTile + wq * 32, n_rows = w.r.nq - first;
+            const bool store = lane < n_rows;
             int b, h, n;
-            row_of(a, w.bk, w.hk, w.r0 + (store ? ri : 0), b, h, n);
-            const int64_t flat = ((int64_t)b * a.H + h) * a.N + n;
+            tile_row(a, w.r, w.hk, store ? first + lane : 0, b, h, n);
+            const int64_t total = (int64_t)a.B * a.H * a.N, flat = ((int64_t)b * a.H + h) * a.N + n;
             const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a NaN sum stays one
             const float lse2 = l == 0.f ? -INFINITY : m_run + log2f(l);
-            const int64_t total = (int64_t)a.B * a.H * a.N;
-#pragma unroll
-            for (int c4 = 0; c4 < D / 32; ++c4) {
-                uint32_t o[32];
-                if (some) {
-                    tmem_ld32(tO + c4 * 32, o);
+            T *o = static_cast<T *>(a.o);
+            auto o_row = [&](int i) {
+                int rb, rh, rn;
+                tile_row(a, w.r, w.hk, first + i, rb, rh, rn);
+                return o + rb * a.oB + rh * a.oH + rn * a.oN;
+            };
+            auto part_row = [&](int i) {
+                int rb, rh, rn;
+                tile_row(a, w.r, w.hk, first + i, rb, rh, rn);
+                return a.part_o + (w.split * total + ((int64_t)rb * a.H + rh) * a.N + rn) * D;
+            };
+            if (some) {
+#pragma unroll 1
+                for (int c = 0; c < D / 64; ++c) {
+                    uint32_t r[64];
+                    tmem_ld32(tO + c * 64, r);
+                    tmem_ld32(tO + c * 64 + 32, r + 32);
                     tmem_wait_ld();
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = 0u;
-                }
-                if (some && c4 == D / 32 - 1) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&o_empty[t]);
-                }
-                if (store) {
-                    float f[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]) * inv;
-                    if (a.splits > 1) {
-                        float *dst = a.part_o + (w.split * total + flat) * D + c4 * 32;
-#pragma unroll
-                        for (int i = 0; i < 32; i += 8) store8(dst + i, f + i);
-                    } else {
-                        T *dst = static_cast<T *>(a.o) + b * a.oB + h * a.oH + n * a.oN + c4 * 32;
-#pragma unroll
-                        for (int i = 0; i < 32; i += 8) store8(dst + i, f + i);
+                    if (c == D / 64 - 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&o_empty[t]);
                     }
+                    float f[64];
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) f[i] = __uint_as_float(r[i]) * inv;
+                    uint4 u[8];
+                    if (a.splits > 1) {
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) u[i] = bits4(f + x * 32 + 4 * i);
+                            store_staged<8>(stage, u, n_rows, [&](int i) { return part_row(i) + c * 64 + x * 32; });
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) u[i] = pack8<T>(f + 8 * i);
+                        store_staged<8>(stage, u, n_rows, [&](int i) { return o_row(i) + c * 64; });
+                    }
+                }
+                fence_async_smem();  // before a TMA load writes the buffer again
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_empty[buf]);
+            } else if (store) {
+                const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                for (int i = 0; i < D; i += 8) {
+                    if (a.splits > 1) store8(part_row(lane) + i, zero);
+                    else store8(o_row(lane) + i, zero);
                 }
             }
             if (store) {
@@ -456,9 +483,9 @@ cudaError_t cross_fwd_error(int32_t *err, bool clear)
 // one 128-key tile (some 1.2 us a CTA).  An item costs its tiles and about two
 // more for its Q rows and epilogue; a split adds a launch (about 3 steps) and
 // the partial outputs' traffic.
-int cross_fwd_splits(int64_t sets, int64_t row_tiles, int64_t M, int64_t rows_total, int D, int sms)
+int cross_fwd_splits(int64_t sets, int64_t pairs, int64_t M, int64_t rows_total, int D, int sms)
 {
-    const int64_t tiles = (M + kTile - 1) / kTile, items = sets * row_tiles;
+    const int64_t tiles = (M + kTile - 1) / kTile, items = sets * pairs;
     int best = 1;
     double least = 0.0;
     for (int64_t s = 1; s <= tiles && s <= 128 && (s == 1 || items * (s - 1) < sms); ++s) {
@@ -474,10 +501,10 @@ int cross_fwd_splits(int64_t sets, int64_t row_tiles, int64_t M, int64_t rows_to
 }
 
 template <typename T>
-static void launch_fwd_t(const CrossArgs &a, int D, int grid, cudaStream_t st)
+static void launch_fwd_t(const CrossArgs &a, const CrossMaps &m, int D, int grid, cudaStream_t st)
 {
-    if (D == 128) cross_fwd_kernel<T, 128><<<grid, kFwdThreads, fwd_smem(128), st>>>(a);
-    else cross_fwd_kernel<T, 64><<<grid, kFwdThreads, fwd_smem(64), st>>>(a);
+    if (D == 128) cross_fwd_kernel<T, 128><<<grid, kFwdThreads, fwd_smem(128), st>>>(a, m);
+    else cross_fwd_kernel<T, 64><<<grid, kFwdThreads, fwd_smem(64), st>>>(a, m);
     count_launches(1);
     if (a.splits > 1) {
         const int64_t threads = (int64_t)a.B * a.H * a.N * (D / 8);
@@ -486,11 +513,11 @@ static void launch_fwd_t(const CrossArgs &a, int D, int grid, cudaStream_t st)
     }
 }
 
-void launch_cross_fwd(const CrossArgs &a, int D, bool f16, int sms, cudaStream_t st)
+void launch_cross_fwd(const CrossArgs &a, const CrossMaps &m, int D, bool f16, int sms, cudaStream_t st)
 {
     const int grid = a.items < sms ? a.items : sms;
-    if (f16) launch_fwd_t<__half>(a, D, grid, st);
-    else launch_fwd_t<__nv_bfloat16>(a, D, grid, st);
+    if (f16) launch_fwd_t<__half>(a, m, D, grid, st);
+    else launch_fwd_t<__nv_bfloat16>(a, m, D, grid, st);
 }
 
 }  // namespace op

@@ -8,20 +8,33 @@
 // query heads of the group and, for keys shared by the batch, its entries.
 //
 // Two tensor-core kernels, one per direction of the sum: cross_dq_kernel owns
-// 128 rows and walks the keys (3 products a tile: S, dP, dQ), cross_dkv_kernel
-// owns 128 keys and walks the rows (4 products: S^T, dP^T, dV, dK).  S and dP
-// are computed twice, 14 D flops a pair instead of 10 D, and in exchange every
+// 128 rows and walks the keys, cross_dkv_kernel owns 128 keys and walks the rows,
+// four products a tile each.  S and dP are computed twice, and in exchange every
 // accumulator stays in TMEM and no result is added up by atomics, so equal
 // calls give equal bits.  (One kernel for both would send a fp32 dQ or dK/dV
-// tile to memory per tile step.)  Bound: the tensor cores, 512 clocks a
-// product of 128 x 128 x 128, against one exponential a pair in each kernel.
+// tile to memory per tile step.)
+//
+// The given o is rounded to 16 bits, and D' = do . o with it: its error is a
+// share of |do| |o|, which all of a row's ds would carry (more than their own
+// rounding, and many times more where the values have a common offset).  The dq
+// kernel therefore sums t_ij = p_ij (dp_ij - D'_i), which sum to D_i - D'_i over
+// a row (held in fp32), next to E_i = sum_j p_ij k_j, and takes
+//   dq_i = scale (sum_j t_ij k_j - (D_i - D'_i) E_i),
+// and the dk/dv kernel after it reads the corrected D_i.
+//
+// Both run the same pipeline over two TMEM buffers X0, X1 of 128 columns: S of
+// step i goes to X[i%2], dP to the other; p and ds (16 bit, 64 columns each)
+// overwrite S.  S of the next step is out as soon as dP has been read, under
+// the ds of this one, and the exponentials of the next step run under the
+// accumulations and dP: 2048 clocks of products a step, with about 500 in
+// which only S is in flight.
 //
 // Rows split over CTAs (few keys, many rows) or keys split (few rows, many
 // keys) leave fp32 partial sums that a join adds in a fixed order.
 //
-// p and ds are rounded to the inputs' 16-bit type as operands of dV, dK, dQ;
-// S, dP, D, lse and all sums are fp32.  Barriers, rings, bounded waits as in
-// cross_attn.cu.
+// p and ds are rounded to the inputs' 16-bit type as operands of the products
+// (the tensor cores take 16-bit operands); S, dP, D, lse and all sums are fp32.
+// Barriers, rings, bounded waits as in cross_attn.cu.
 #include "cross_common.cuh"
 
 namespace scope {
@@ -33,15 +46,13 @@ static __device__ int32_t g_cross_bwd_err[4];
 
 constexpr int kBwdThreads = 384;
 constexpr int kT = 128;      // rows or keys of a tile
-constexpr int kQRing = 3;    // dq kernel: Q, dO tiles in flight
-constexpr int kKvRing = 4;   // dq kernel: K, V tiles in flight
-constexpr int kRowRing = 5;  // dk/dv kernel: Q, dO tiles in flight
+constexpr int kTiles = 7;    // tiles in shared memory, both kernels
 
-constexpr size_t dq_smem(int D) { return (size_t)(kQRing + kKvRing) * kT * D * 2 + 1024; }
-// tiles, three row tiles of nlse and two of ndelta, barriers.  At D = 128 that
-// leaves no room to align the base by hand (227 KB a block), so the kernel has
-// no static shared memory and checks that its base is aligned.
-constexpr size_t dkv_smem(int D) { return (size_t)(2 + kRowRing) * kT * D * 2 + 5 * kT * 4 + 256; }
+// Tiles, 5 x 128 floats, barriers.  At D = 128 that leaves no room to align the
+// base by hand (227 KB a block), so the kernels have no static shared memory and
+// check that their base is aligned.
+constexpr int kFloats = 5 * kT;
+constexpr size_t bwd_smem(int D) { return (size_t)kTiles * kT * D * 2 + kFloats * 4 + 256; }
 
 __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b)
 {
@@ -50,9 +61,47 @@ __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b)
     return d;
 }
 
-// A-operand column of 16-element step k: each half of the warpgroups' 64
-// packed values sits at the start of its own half of the fp32 columns.
+// Column of 16-element step k of p (ds: 32 further on) as an A operand: the 64
+// values of each half of the warps sit, packed, in the half's own columns of S.
 __device__ __forceinline__ uint32_t half_col(int k) { return (uint32_t)((k >> 2) * 64 + (k & 3) * 8); }
+
+// rows x cols = A B^T of two [128][D] tiles.
+template <typename T, int D>
+__device__ __forceinline__ void tile_product(uint32_t d, uint32_t a_smem, uint32_t b_smem)
+{
+    const uint32_t id = idesc16<T>(kT, false);
+    const uint64_t da = sw128_desc(a_smem, 16, 1024), db = sw128_desc(b_smem, 16, 1024);
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+        const uint64_t o = (uint64_t)(((k >> 2) * (kT * 128) + (k & 3) * 32) >> 4);
+        mma_ss(d, da + o, db + o, id, k > 0);
+    }
+}
+
+// d (+)= P B, P [128][128] packed at TMEM column p, B a [128][D] tile.
+template <typename T, int D>
+__device__ __forceinline__ void tile_accumulate(uint32_t d, uint32_t p, uint32_t b_smem, bool first)
+{
+    const uint32_t id = idesc16<T>(D, true);
+    const uint64_t db = sw128_desc(b_smem, kT * 128, 1024);
+#pragma unroll
+    for (int k = 0; k < kT / 16; ++k)
+        mma_ts(d, p + half_col(k), db + (uint64_t)((k * 2048) >> 4), id, !first || k > 0);
+}
+
+// 64 values as 32 packed columns.
+template <typename T>
+__device__ __forceinline__ void store_half(uint32_t col, const uint32_t *r)
+{
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            pk[i] = pack2(T(), __uint_as_float(r[c * 32 + 2 * i]), __uint_as_float(r[c * 32 + 2 * i + 1]));
+        tmem_st16(col + c * 16, pk);
+    }
+}
 
 __device__ __forceinline__ void bwd_prologue(int warp, uint32_t *tmem_base)
 {
@@ -75,51 +124,65 @@ __device__ __forceinline__ void bwd_epilogue(int warp, uint32_t tmem)
     }
 }
 
-// nlse and ndelta of every row of every key set, in the sets' row order.
-template <typename T>
-__global__ void __launch_bounds__(256) cross_rows_kernel(const __grid_constant__ CrossArgs a, int D)
+// nlse and ndelta (from the rounded o) of every row: one block per row tile.
+// Bound by HBM (o and do are read once).
+template <typename T, int D>
+__global__ void __launch_bounds__(256) cross_rows_kernel(const __grid_constant__ CrossArgs a)
 {
-    const int lpr = D / 8;
-    const int64_t at = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / lpr;
-    const int c8 = threadIdx.x % lpr;
-    if (at >= (int64_t)a.sets * a.rows_pad) return;  // whole row groups of lanes
-    const int set = (int)(at / a.rows_pad), r = (int)(at % a.rows_pad);
-    const unsigned lanes = (lpr == 16 ? 0xffffu : 0xffu) << ((threadIdx.x & 31) & ~(lpr - 1));
-    float sum = 0.f, nl = -INFINITY;
-    if (r < a.rows) {
-        int b, h, n;
-        row_of(a, set / a.Hk, set % a.Hk, r, b, h, n);
-        float o[8], d[8];
-        load8(static_cast<const T *>(a.o) + b * a.oB + h * a.oH + n * a.oN + c8 * 8, o);
-        load8(static_cast<const T *>(a.dout) + b * a.dB + h * a.dH + n * a.dN + c8 * 8, d);
+    constexpr int LPR = D / 8, RPP = 256 / LPR;  // lanes a row, rows a pass
+    const int set = blockIdx.x / a.tiles, rt = blockIdx.x % a.tiles, hk = set % a.Hk;
+    const RowTile w = row_tile<kT>(a, set / a.Hk, hk, rt);
+    const int c8 = threadIdx.x % LPR, row0 = threadIdx.x / LPR;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(o[i], d[i], sum);
-        const float lse = a.lse[((int64_t)b * a.H + h) * a.N + n];
-        if (lse != -INFINITY) nl = -lse * 1.4426950408889634f;
-    }
-    for (int o = lpr >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(lanes, sum, o);
-    if (c8 == 0) {
-        a.nlse[at] = nl;
-        a.ndelta[at] = -sum;
+    for (int half = 0; half < 2; ++half) {
+        float sum[kT / RPP / 2], nl[kT / RPP / 2];
+#pragma unroll
+        for (int x = 0; x < kT / RPP / 2; ++x) {
+            const int i = (half * (kT / RPP / 2) + x) * RPP + row0;
+            sum[x] = 0.f;
+            nl[x] = -INFINITY;
+            if (i < w.nq) {
+                int b, h, n;
+                tile_row(a, w, hk, i, b, h, n);
+                float o[8], d[8];
+                load8(static_cast<const T *>(a.o) + b * a.oB + h * a.oH + n * a.oN + c8 * 8, o);
+                load8(static_cast<const T *>(a.dout) + b * a.dB + h * a.dH + n * a.dN + c8 * 8, d);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum[x] = fmaf(o[e], d[e], sum[x]);
+                const float lse = a.lse[((int64_t)b * a.H + h) * a.N + n];
+                if (lse != -INFINITY) nl[x] = -lse * 1.4426950408889634f;
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < kT / RPP / 2; ++x) {
+#pragma unroll
+            for (int o = LPR >> 1; o > 0; o >>= 1) sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], o);
+            if (c8 == 0) {
+                const int64_t at = (int64_t)blockIdx.x * kT + (half * (kT / RPP / 2) + x) * RPP + row0;
+                a.nlse[at] = nl[x];
+                a.ndelta[at] = -sum[x];
+            }
+        }
     }
 }
 
 // ---------------------------------------------------------------- dq
 struct DqItem {
-    int bk, hk, set, r0, nq, t0, t1, nk, split;
+    int bk, hk, t0, t1, nk, split;
+    int64_t at;  // padded row of its first row
+    RowTile r;
 };
 
 __device__ __forceinline__ DqItem dq_item(const CrossArgs &a, int item)
 {
     DqItem w;
-    const int tiles = a.rows_pad / kT;
-    const int rt = item % tiles, rest = item / tiles;
+    const int rt = item % a.tiles, rest = item / a.tiles;
     w.split = rest % a.dq_splits;
-    w.set = rest / a.dq_splits;
-    w.bk = w.set / a.Hk;
-    w.hk = w.set % a.Hk;
-    w.r0 = rt * kT;
-    w.nq = min(kT, a.rows - w.r0);
+    const int set = rest / a.dq_splits;
+    w.bk = set / a.Hk;
+    w.hk = set % a.Hk;
+    w.r = row_tile<kT>(a, w.bk, w.hk, rt);
+    w.at = ((int64_t)set * a.tiles + rt) * kT;
     w.nk = keys_of(a, w.bk);
     const int kt = (w.nk + kT - 1) / kT;
     w.t0 = (int)((int64_t)kt * w.split / a.dq_splits);
@@ -127,167 +190,171 @@ __device__ __forceinline__ DqItem dq_item(const CrossArgs &a, int item)
     return w;
 }
 
-// One persistent CTA per SM; item = 128 rows of a key set.  TMEM: S in two
-// buffers [0,128) [128,256), so S(j+1) is computed under the softmax of j; dP
-// [256,384); dQ [384,384+D).  Warps 0-3 take the keys 0-63 of a tile, warps
-// 4-7 the keys 64-127, one thread per row and half; ds (16 bit) overwrites the
-// half's own part of S.  S and dP of step j+1 are out before ds of j is awaited,
-// so the warps may arrive for both steps before the issuer looks: one ds_full
-// barrier per S buffer (a single one would have passed the awaited phase twice).
+// A CTA's key tiles in order, over its items.
+struct DqStep {
+    int item, j;
+    DqItem w;
+    __device__ __forceinline__ bool seek(const CrossArgs &a, int from, int items)
+    {
+        for (item = from; item < items; item += gridDim.x) {
+            w = dq_item(a, item);
+            j = w.t0;
+            if (w.t0 < w.t1) return true;
+        }
+        return false;
+    }
+    __device__ __forceinline__ bool next(const CrossArgs &a, int items)
+    {
+        return ++j < w.t1 || seek(a, item + gridDim.x, items);
+    }
+};
+
+// One persistent CTA per SM; item = 128 rows of a key set and a key range.  TMEM:
+// X0 [0,128), X1 [128,256), sum t k [256,256+D), sum p k [384,384+D).  Shared
+// memory: 2 Q tiles (the next item's comes early; dq leaves through it), 1 dO
+// tile, rings of 3 K and 1 V tiles.  Warps 0-3 take the keys 0-63 of a tile,
+// warps 4-7 the keys 64-127, one thread per row and half; warps 8, 9, 10 load
+// Q and dO, K, V; warp 11 issues.
 template <typename T, int D>
-__global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_constant__ CrossArgs a, int items)
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    cross_dq_kernel(const __grid_constant__ CrossArgs a, const __grid_constant__ CrossMaps m, int items)
 {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    unsigned char *sm = (unsigned char *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     constexpr int TB = kT * D * 2;
-    unsigned char *sR = sm, *sKV = sm + kQRing * TB;
-    __shared__ uint64_t r_full[kQRing], r_empty[kQRing], kv_full[kKvRing], kv_empty[kKvRing], s_full[2], dp_full, dp_read,
-        ds_full[2], dq_full, dq_empty;
-    __shared__ uint32_t tmem_base_sh;
-    __shared__ int abort_sh;
+    const uint32_t sQ = smem_u32(smem_raw), sO = sQ + 2 * TB, sK = sQ + 3 * TB, sV = sQ + 6 * TB;
+    float *s_delta = reinterpret_cast<float *>(smem_raw + kTiles * TB);  // [2 items][2 halves][kT]
+    struct Barriers {
+        uint64_t q_full[2], q_empty[2], o_full, o_empty, k_full[3], k_empty[3], v_full, v_empty;
+        uint64_t s_full, dp_full, dp_read, ds_full, dq_full, delta_full[4];
+        uint32_t tmem_base;
+        int abort;
+    };
+    static_assert(sizeof(Barriers) <= 256, "room kept in bwd_smem");
+    Barriers &bar = *reinterpret_cast<Barriers *>(smem_raw + kTiles * TB + kFloats * 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (sQ & 1023u) {  // uniform
+        if (threadIdx.x == 0) set_error(g_cross_bwd_err, kErrRange, 0x70);
+        return;
+    }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kQRing; ++i) {
-            mbar_init(&r_full[i], 1);
-            mbar_init(&r_empty[i], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.q_full[i], 1);
+            mbar_init(&bar.q_empty[i], 8);
         }
-        for (int i = 0; i < kKvRing; ++i) {
-            mbar_init(&kv_full[i], 2);
-            mbar_init(&kv_empty[i], 1);
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(&bar.k_full[i], 1);
+            mbar_init(&bar.k_empty[i], 1);
         }
-        mbar_init(&s_full[0], 1);
-        mbar_init(&s_full[1], 1);
-        mbar_init(&dp_full, 1);
-        mbar_init(&dp_read, 8);
-        mbar_init(&ds_full[0], 8);
-        mbar_init(&ds_full[1], 8);
-        mbar_init(&dq_full, 1);
-        mbar_init(&dq_empty, 8);
-        abort_sh = 0;
+        for (int i = 0; i < 4; ++i) mbar_init(&bar.delta_full[i], 2);
+        mbar_init(&bar.o_full, 1);
+        mbar_init(&bar.o_empty, 1);
+        mbar_init(&bar.v_full, 1);
+        mbar_init(&bar.v_empty, 1);
+        mbar_init(&bar.s_full, 1);
+        mbar_init(&bar.dp_full, 1);
+        mbar_init(&bar.dp_read, 8);
+        mbar_init(&bar.ds_full, 8);
+        mbar_init(&bar.dq_full, 1);
+        bar.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    bwd_prologue(warp, &tmem_base_sh);
-    const uint32_t tmem = tmem_base_sh;
-    const Waiter wait{&abort_sh, g_cross_bwd_err};
+    bwd_prologue(warp, &bar.tmem_base);
+    const uint32_t tmem = bar.tmem_base;
+    const Waiter wait{&bar.abort, g_cross_bwd_err};
 
     if (warp == 8) {
         // ------------------------------------------------------------ Q, dO rows
-        RingFill<kQRing> ring(r_full, r_empty);
+        int qi = 0;
+        bool ok = true;
         for (int item = blockIdx.x; item < items; item += gridDim.x) {
             const DqItem w = dq_item(a, item);
             if (w.t0 == w.t1) continue;
-            if (!ring.acquire(wait, 0x50)) break;
-            copy_rows<T, D>(a, w.bk, w.hk, w.r0, w.nq, kT, static_cast<const T *>(a.q), a.qB, a.qH, a.qN,
-                            smem_u32(sR + ring.slot * TB), lane, 32);
-            ring.issued();
-            if (!ring.acquire(wait, 0x50)) break;
-            copy_rows<T, D>(a, w.bk, w.hk, w.r0, w.nq, kT, static_cast<const T *>(a.dout), a.dB, a.dH, a.dN,
-                            smem_u32(sR + ring.slot * TB), lane, 32);
-            ring.issued();
+            const int buf = qi & 1;
+            if (qi >= 2 && !(ok = wait.warp(&bar.q_empty[buf], ((qi >> 1) - 1) & 1, 0x50))) break;
+            load_rows<T, D>(a, w.r, w.hk, 1, &m.q, a.q, a.qB, a.qH, a.qN, sQ + buf * TB, &bar.q_full[buf]);
+            ++qi;
+            if (qi >= 2 && !(ok = wait.warp(&bar.o_empty, (qi - 2) & 1, 0x50))) break;
+            load_rows<T, D>(a, w.r, w.hk, 1, &m.d, a.dout, a.dB, a.dH, a.dN, sO, &bar.o_full);
         }
-        ring.flush();
+        if (!ok) {  // the last dO has been waited for (it is free) or belongs to the item before
+            for (int i = max(0, qi - 2); i < qi; ++i) drain(&bar.q_full[i & 1], (i >> 1) & 1);
+            if (qi >= 2) drain(&bar.o_full, (qi - 2) & 1);
+        }
     } else if (warp == 9 || warp == 10) {
-        // ------------------------------------------------------------ K, V rows
-        const int tid = threadIdx.x - 9 * 32;
-        RingFill<kKvRing> ring(kv_full, kv_empty);
-        KeyTile<T, D, 64> tile;
-        bool ok = true;
-        for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
-            const DqItem w = dq_item(a, item);
-            const T *k = static_cast<const T *>(a.k) + w.bk * a.kB + w.hk * a.kH;
-            const T *v = static_cast<const T *>(a.v) + w.bk * a.vB + w.hk * a.vH;
-            const int32_t *list = a.idx ? a.idx + (int64_t)w.bk * a.M : nullptr;
-            for (int j = w.t0; j < w.t1; ++j) {
-                tile.load(list, w.nk, j, tid);
-                if (!(ok = ring.acquire(wait, 0x51))) break;
-                tile.copy(k, a.kN, smem_u32(sKV + ring.slot * TB), tid);
-                ring.issued();
-                if (!(ok = ring.acquire(wait, 0x51))) break;
-                tile.copy(v, a.vN, smem_u32(sKV + ring.slot * TB), tid);
-                ring.issued();
-            }
-        }
-        ring.flush();
-    } else if (warp == 11) {
-        // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            const uint32_t id_s = idesc16<T>(kT, false), id_q = idesc16<T>(D, true);
-            const uint64_t dr = sw128_desc(smem_u32(sR), 16, 1024);
-            const uint64_t dkv = sw128_desc(smem_u32(sKV), 16, 1024);
-            const uint64_t dmn = sw128_desc(smem_u32(sKV), kT * 128, 1024);
-            RingRead<kQRing> rr;
-            RingRead<kKvRing> kv;
-            int ns = 0, nd = 0, no = 0;  // steps issued in all (S buffer), dP reads awaited, dQ tiles done
-            auto product = [&](uint32_t d, int rslot, int kvslot) {  // d = rows x keys
-                const uint64_t ar = dr + (uint64_t)((rslot * TB) >> 4), bk = dkv + (uint64_t)((kvslot * TB) >> 4);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint64_t o = (uint64_t)(((k >> 2) * (kT * 128) + (k & 3) * 32) >> 4);
-                    mma_ss(d, ar + o, bk + o, id_s, k > 0);
-                }
-            };
+        // ------------------------------------------------------------ K rows, V rows
+        auto fill = [&](auto &ring, const CUtensorMap *map, const void *src, int64_t sB, int64_t sH, int64_t sN,
+                        uint32_t smem) {
             bool ok = true;
             for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
                 const DqItem w = dq_item(a, item);
-                if (w.t0 == w.t1) continue;
-                const int qs = rr.slot;
-                if (!(ok = wait(&r_full[qs], rr.use & 1, 0x52))) break;
-                rr.next();
-                const int os = rr.slot, o_use = rr.use;
-                rr.next();
-                int ks = kv.slot;  // K of the current step
-                if (!(ok = wait(&kv_full[ks], kv.use & 1, 0x53))) break;
-                kv.next();
-                tc_fence_after();
-                product(tmem + (ns & 1) * 128, qs, ks);
-                mma_commit(&s_full[ns & 1]);
-                if (w.t0 + 1 == w.t1) mma_commit(&r_empty[qs]);
-                if (!(ok = wait(&r_full[os], o_use & 1, 0x54) && wait(&kv_full[kv.slot], kv.use & 1, 0x55))) break;
-                // the softmax has read the dP before this one
-                if (nd > 0 && !(ok = wait(&dp_read, (nd - 1) & 1, 0x56))) break;
-                tc_fence_after();
-                product(tmem + 256, os, kv.slot);
-                mma_commit(&dp_full);
-                mma_commit(&kv_empty[kv.slot]);
-                if (w.t0 + 1 == w.t1) mma_commit(&r_empty[os]);
-                kv.next();
-                ++nd;
+                const T *base = static_cast<const T *>(src) + w.bk * sB + w.hk * sH;
+                const int32_t *list = a.idx ? a.idx + (int64_t)w.bk * a.M : nullptr;
                 for (int j = w.t0; j < w.t1; ++j) {
-                    const bool more = j + 1 < w.t1, last = j + 2 == w.t1;
-                    const int cur = ns & 1;
-                    int kn = 0;
-                    if (more) {
-                        kn = kv.slot;
-                        if (!(ok = wait(&kv_full[kn], kv.use & 1, 0x57))) break;
-                        kv.next();
-                        tc_fence_after();
-                        product(tmem + (cur ^ 1) * 128, qs, kn);
-                        mma_commit(&s_full[cur ^ 1]);
-                        if (last) mma_commit(&r_empty[qs]);
-                        if (!(ok = wait(&kv_full[kv.slot], kv.use & 1, 0x58) && wait(&dp_read, (nd - 1) & 1, 0x59))) break;
-                        tc_fence_after();
-                        product(tmem + 256, os, kv.slot);
-                        mma_commit(&dp_full);
-                        mma_commit(&kv_empty[kv.slot]);
-                        if (last) mma_commit(&r_empty[os]);
-                        kv.next();
-                        ++nd;
+                    if (!(ok = ring.acquire(wait, 0x51))) break;
+                    const uint32_t dst = smem + ring.slot * TB;
+                    if (tma_keys(a, w.nk, j)) {
+                        ring.template tma<D>(true, dst, map, j * kT, w.hk, w.bk);
+                    } else {
+                        copy_keys<T, D, 32>(list, w.nk, j, base, sN, dst, lane);
+                        ring.issued();
                     }
-                    if (!(ok = wait(&ds_full[cur], (ns >> 1) & 1, 0x5a))) break;
-                    // the previous item's dQ has been read
-                    if (j == w.t0 && no > 0 && !(ok = wait(&dq_empty, (no - 1) & 1, 0x5b))) break;
-                    tc_fence_after();
-                    const uint64_t bk = dmn + (uint64_t)((ks * TB) >> 4);
-#pragma unroll
-                    for (int k = 0; k < kT / 16; ++k)
-                        mma_ts(tmem + 384, tmem + cur * 128 + half_col(k), bk + (uint64_t)((k * 2048) >> 4), id_q,
-                               j > w.t0 || k > 0);
-                    mma_commit(&kv_empty[ks]);
-                    if (!more) mma_commit(&dq_full);
-                    ks = kn;
-                    ++ns;
                 }
-                ++no;
+            }
+            ring.finish(!ok);
+        };
+        if (warp == 9) {
+            RingFill<3> ring(bar.k_full, bar.k_empty);
+            fill(ring, &m.k, a.k, a.kB, a.kH, a.kN, sK);
+        } else {
+            RingFill<1> ring(&bar.v_full, &bar.v_empty);
+            fill(ring, &m.v, a.v, a.vB, a.vH, a.vN, sV);
+        }
+    } else if (warp == 11) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            RingRead<3> kr;
+            DqStep cur, nxt;
+            int ns = 0, qi = 0;  // steps, items begun
+            auto issue_s = [&](const DqStep &st, int step, int &slot) {
+                const int item = st.j == st.w.t0 ? qi++ : qi - 1;
+                if (!wait(&bar.q_full[item & 1], (item >> 1) & 1, 0x52)) return false;
+                slot = kr.slot;
+                if (!wait(&bar.k_full[slot], kr.use & 1, 0x53)) return false;
+                kr.next();
+                tc_fence_after();
+                tile_product<T, D>(tmem + (step & 1) * 128, sQ + (item & 1) * TB, sK + slot * TB);
+                mma_commit(&bar.s_full);
+                return true;
+            };
+            auto issue_dp = [&](const DqStep &st, int step) {
+                if (!wait(&bar.o_full, (qi - 1) & 1, 0x54) || !wait(&bar.v_full, step & 1, 0x55)) return false;
+                tc_fence_after();
+                tile_product<T, D>(tmem + ((step & 1) ^ 1) * 128, sO, sV);
+                mma_commit(&bar.dp_full);
+                mma_commit(&bar.v_empty);
+                if (st.j + 1 == st.w.t1) mma_commit(&bar.o_empty);
+                return true;
+            };
+            int ks = 0, kn = 0;
+            bool more = cur.seek(a, blockIdx.x, items);
+            bool ok = more && issue_s(cur, 0, ks) && issue_dp(cur, 0);
+            while (ok && more) {
+                nxt = cur;
+                more = nxt.next(a, items);
+                // dP of this step has been read: the buffer is free for the next S
+                if (more && !(ok = wait(&bar.dp_read, ns & 1, 0x56) && issue_s(nxt, ns + 1, kn))) break;
+                if (!(ok = wait(&bar.ds_full, ns & 1, 0x57))) break;
+                tc_fence_after();
+                const uint32_t p = tmem + (ns & 1) * 128;
+                const bool first = cur.j == cur.w.t0;
+                tile_accumulate<T, D>(tmem + 256, p + 32, sK + ks * TB, first);
+                tile_accumulate<T, D>(tmem + 384, p, sK + ks * TB, first);
+                mma_commit(&bar.k_empty[ks]);
+                if (cur.j + 1 == cur.w.t1) mma_commit(&bar.dq_full);
+                if (more && !(ok = issue_dp(nxt, ns + 1))) break;
+                cur = nxt;
+                ks = kn;
+                ++ns;
             }
         }
         __syncwarp();
@@ -295,18 +362,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_c
         // ------------------------------------------------------------ softmax and epilogue
         const int half = warp >> 2, wq = warp & 3, row = wq * 32 + lane;
         const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
-        int ns = 0, no = 0;
+        int ns = 0, qi = 0;
         bool ok = true;
-        const uint64_t scp = f2pack(a.scale * 1.4426950408889634f, a.scale * 1.4426950408889634f);
+        const uint64_t scp = f2pack(a.scale_log2, a.scale_log2);
         for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
             const DqItem w = dq_item(a, item);
-            const int64_t at = (int64_t)w.set * a.rows_pad + w.r0 + row;
-            const float nl = a.nlse[at], nd = a.ndelta[at];
+            const float nl = a.nlse[w.at + row], nd = a.ndelta[w.at + row];
             const uint64_t nlp = f2pack(nl, nl), ndp = f2pack(nd, nd);
-            for (int j = w.t0; j < w.t1; ++j) {
+            uint64_t dA = 0ull, dB = 0ull;
+            for (int j = w.t0; j < w.t1; ++j, ++ns) {
                 const uint32_t tS = tmem + lane_off + (ns & 1) * 128 + half * 64;
-                const uint32_t tP = tmem + lane_off + 256 + half * 64;
-                if (!(ok = wait.warp(&s_full[ns & 1], (ns >> 1) & 1, 0x5c))) break;
+                const uint32_t tP = tmem + lane_off + ((ns & 1) ^ 1) * 128 + half * 64;
+                if (!(ok = wait.warp(&bar.s_full, ns & 1, 0x58))) break;
                 tc_fence_after();
                 uint32_t r[64];
                 tmem_ld32(tS, r);
@@ -325,7 +392,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_c
                     for (int i = 0; i < 64; ++i)
                         if (i >= valid) r[i] = 0u;
                 }
-                if (!(ok = wait.warp(&dp_full, ns & 1, 0x5d))) break;
+                store_half<T>(tS, r);
+                if (!(ok = wait.warp(&bar.dp_full, ns & 1, 0x59))) break;
                 tc_fence_after();
                 uint32_t d[64];
                 tmem_ld32(tP, d);
@@ -333,75 +401,128 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dq_kernel(const __grid_c
                 tmem_wait_ld();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&dp_read);
+                if (lane == 0) mbar_arrive(&bar.dp_read);
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int e = c * 32 + 2 * i;
-                        float x0, x1;
-                        f2unpack(fmul2(f2pack(__uint_as_float(r[e]), __uint_as_float(r[e + 1])),
-                                       fadd2(f2pack(__uint_as_float(d[e]), __uint_as_float(d[e + 1])), ndp)),
-                                 x0, x1);
-                        pk[i] = pack2(T(), x0, x1);
-                    }
-                    tmem_st16(tS + c * 16, pk);
+                for (int i = 0; i < 32; ++i) {
+                    const uint64_t t2 = fmul2(f2pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])),
+                                              fadd2(f2pack(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1])), ndp));
+                    if (i & 1) dB = fadd2(dB, t2);
+                    else dA = fadd2(dA, t2);
+                    float x0, x1;
+                    f2unpack(t2, x0, x1);
+                    d[2 * i] = __float_as_uint(x0);
+                    d[2 * i + 1] = __float_as_uint(x1);
                 }
+                store_half<T>(tS + 32, d);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ds_full[ns & 1]);
-                ++ns;
+                if (lane == 0) mbar_arrive(&bar.ds_full);
             }
             if (!ok) break;
-            const bool some = w.t0 < w.t1;
-            if (some) {
-                if (!(ok = wait.warp(&dq_full, no & 1, 0x5e))) break;
-                ++no;
-                tc_fence_after();
-            }
-            const bool store = row < w.nq;
+            const int n_rows = w.r.nq - wq * 32;
+            const bool store = lane < n_rows;
             int b, h, n;
-            row_of(a, w.bk, w.hk, w.r0 + (store ? row : 0), b, h, n);
+            tile_row(a, w.r, w.hk, store ? row : 0, b, h, n);
             const int64_t total = (int64_t)a.B * a.H * a.N, flat = ((int64_t)b * a.H + h) * a.N + n;
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-                const int col = half * (D / 2) + c * 32;
-                uint32_t o[32];
-                if (some) {
-                    tmem_ld32(tmem + lane_off + 384 + col, o);
-                    tmem_wait_ld();
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = 0u;
-                }
-                if (some && c == D / 64 - 1) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&dq_empty);
-                }
+            T *dq = static_cast<T *>(a.dq);
+            auto dq_row = [&](int i) {
+                int rb, rh, rn;
+                tile_row(a, w.r, w.hk, wq * 32 + i, rb, rh, rn);
+                return dq + rb * a.dqB + rh * a.dqH + rn * a.dqN + half * (D / 2);
+            };
+            auto part_row = [&](float *part, int i) {
+                int rb, rh, rn;
+                tile_row(a, w.r, w.hk, wq * 32 + i, rb, rh, rn);
+                return part + (w.split * total + ((int64_t)rb * a.H + rh) * a.N + rn) * D + half * (D / 2);
+            };
+            if (w.t0 == w.t1) {  // no keys
                 if (store) {
-                    float f[32];
+                    const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                    for (int i = 0; i < D / 2; i += 8) {
+                        if (a.dq_splits > 1) {
+                            store8(part_row(a.part_t, lane) + i, zero);
+                            store8(part_row(a.part_e, lane) + i, zero);
+                        } else {
+                            store8(dq_row(lane) + i, zero);
+                        }
+                    }
+                    if (a.dq_splits > 1 && half == 0) a.part_delta[w.split * total + flat] = 0.f;
+                }
+                continue;
+            }
+            // D - D' of the row: both halves' sums
+            float d0, d1, d2, d3;
+            f2unpack(dA, d0, d1);
+            f2unpack(dB, d2, d3);
+            float delta = (d0 + d2) + (d1 + d3);
+            // two buffers in turn: a warp may be in the next item before its pair has read this one's (but not in
+            // the one after, whose dP waits for the pair's ds)
+            float *pair = s_delta + (qi & 1) * 2 * kT + row;
+            pair[half * kT] = delta;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.delta_full[wq]);
+            if (!(ok = wait.warp(&bar.delta_full[wq], qi & 1, 0x5a))) break;
+            delta = pair[0] + pair[kT];
+            if (half == 0) {
+                if (a.dq_splits > 1) {
+                    if (store) a.part_delta[w.split * total + flat] = delta;
+                } else {
+                    a.ndelta[w.at + row] = nd - delta;
+                }
+            }
+            if (!(ok = wait.warp(&bar.dq_full, qi & 1, 0x5b))) break;
+            tc_fence_after();
+            const uint32_t stage = sQ + (qi & 1) * TB + warp * (TB / 8);
+            if (a.dq_splits > 1) {
+#pragma unroll 1
+                for (int x = 0; x < 2 * (D / 64); ++x) {
+                    const int e = x & 1, c = x >> 1;
+                    uint32_t r[32];
+                    tmem_ld32(tmem + lane_off + 256 + e * 128 + half * (D / 2) + c * 32, r);
+                    tmem_wait_ld();
+                    // fp32: 16 columns a pass at D = 64, where a warp has 2 KB to stage in
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]) * a.scale;
-                    if (a.dq_splits > 1) {
-                        float *dst = a.part_dq + (w.split * total + flat) * D + col;
+                    for (int y = 0; y < 128 / D; ++y) {
+                        constexpr int CH = D / 16;
+                        uint4 u[CH];
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) store8(dst + i, f + i);
-                    } else {
-                        T *dst = static_cast<T *>(a.dq) + b * a.dqB + h * a.dqH + n * a.dqN + col;
-#pragma unroll
-                        for (int i = 0; i < 32; i += 8) store8(dst + i, f + i);
+                        for (int i = 0; i < CH; ++i)
+                            u[i] = make_uint4(r[(y * CH + i) * 4], r[(y * CH + i) * 4 + 1], r[(y * CH + i) * 4 + 2],
+                                              r[(y * CH + i) * 4 + 3]);
+                        store_staged<CH>(stage, u, n_rows, [&](int i) {
+                            return part_row(e ? a.part_e : a.part_t, i) + c * 32 + y * CH * 4;
+                        });
                     }
                 }
+            } else {
+                uint4 u[D / 16];
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    uint32_t r[32], e[32];
+                    tmem_ld32(tmem + lane_off + 256 + half * (D / 2) + c * 32, r);
+                    tmem_ld32(tmem + lane_off + 384 + half * (D / 2) + c * 32, e);
+                    tmem_wait_ld();
+                    float f[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        f[i] = fmaf(-delta, __uint_as_float(e[i]), __uint_as_float(r[i])) * a.scale;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) u[c * 4 + i] = pack8<T>(f + 8 * i);
+                }
+                store_staged<D / 16>(stage, u, n_rows, dq_row);
             }
+            tc_fence_before();
+            fence_async_smem();  // before a TMA load writes the Q buffer again
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.q_empty[qi & 1]);
+            ++qi;
         }
     }
     bwd_epilogue(warp, tmem);
 }
 
-// dq = sum of the key ranges' parts.
+// dq from the key ranges' parts, and the corrected ndelta.
 template <typename T>
 __global__ void __launch_bounds__(256) cross_dq_join_kernel(const __grid_constant__ CrossArgs a, int D)
 {
@@ -410,65 +531,75 @@ __global__ void __launch_bounds__(256) cross_dq_join_kernel(const __grid_constan
     const int64_t row = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / lpr;
     const int c8 = threadIdx.x % lpr;
     if (row >= total) return;
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, e[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, delta = 0.f;
 #pragma unroll 4
     for (int s = 0; s < a.dq_splits; ++s) {
-        float x[8];
-        load8(a.part_dq + (s * total + row) * D + c8 * 8, x);
+        float x[8], y[8];
+        load8(a.part_t + (s * total + row) * D + c8 * 8, x);
+        load8(a.part_e + (s * total + row) * D + c8 * 8, y);
+        delta += a.part_delta[s * total + row];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] += x[i];
+        for (int i = 0; i < 8; ++i) {
+            t[i] += x[i];
+            e[i] += y[i];
+        }
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = fmaf(-delta, e[i], t[i]) * a.scale;
     const int64_t bh = row / a.N, n = row % a.N;
-    store8(static_cast<T *>(a.dq) + (bh / a.H) * a.dqB + (bh % a.H) * a.dqH + n * a.dqN + c8 * 8, acc);
+    store8(static_cast<T *>(a.dq) + (bh / a.H) * a.dqB + (bh % a.H) * a.dqH + n * a.dqN + c8 * 8, t);
+    if (c8 == 0) a.ndelta[padded_row(a, (int)(bh / a.H), (int)(bh % a.H), (int)n)] -= delta;
 }
 
 // ---------------------------------------------------------------- dk, dv
-// One CTA per (key set, 128 keys, row range).  TMEM: S^T [0,128), dP^T
-// [128,256), dV [256,256+D), dK [384,384+D).  P^T and dS^T (16 bit) overwrite
-// S^T and dP^T.  Two phases alternate: dV(i) and S^T(i+1) run under the ds of
-// row tile i, dK(i) and dP^T(i+1) under the exponentials of i+1.  Warps 0-3
-// take the rows 0-63 of a row tile, warps 4-7 the rows 64-127, one thread per
-// key and half.
+// One CTA per (key set, 128 keys, row range); keys are the rows of its products:
+// S^T = K Q^T and dP^T = V dO^T in X0, X1, dV [256,256+D), dK [384,384+D).
+// Shared memory: K, V, rings of 3 Q and 2 dO tiles with the rows' nlse, ndelta.
+// Warps 0-3 take the rows 0-63 of a row tile, warps 4-7 the rows 64-127, one
+// thread per key and half; warps 8, 9, 10 load K and V, Q, dO; warp 11 issues.
 template <typename T, int D>
-__global__ void __launch_bounds__(kBwdThreads, 1) cross_dkv_kernel(const __grid_constant__ CrossArgs a, int key_tiles)
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    cross_dkv_kernel(const __grid_constant__ CrossArgs a, const __grid_constant__ CrossMaps m, int key_tiles)
 {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    unsigned char *sm = smem_raw;
     constexpr int TB = kT * D * 2;
-    unsigned char *sK = sm, *sV = sm + TB, *sR = sm + 2 * TB;
-    float *s_nl = reinterpret_cast<float *>(sm + (2 + kRowRing) * TB);  // [3][kT]
-    float *s_nd = s_nl + 3 * kT;                                        // [2][kT]
+    const uint32_t sK = smem_u32(smem_raw), sV = sK + TB, sQ = sK + 2 * TB, sO = sK + 5 * TB;
+    float *s_nl = reinterpret_cast<float *>(smem_raw + kTiles * TB);  // [3][kT]
+    float *s_nd = s_nl + 3 * kT;                                      // [2][kT]
     struct Barriers {
-        uint64_t k_full, r_full[kRowRing], r_empty[kRowRing], s_full, dp_full, p_full, ds_full, acc_full;
+        uint64_t kv_full, q_full[3], q_empty[3], o_full[2], o_empty[2], s_full, dp_full, dp_read, ds_full, acc_full;
         uint32_t tmem_base;
         int abort;
     };
-    static_assert(sizeof(Barriers) <= 256, "room kept in dkv_smem");
-    Barriers &bar = *reinterpret_cast<Barriers *>(s_nd + 2 * kT);
+    static_assert(sizeof(Barriers) <= 256, "room kept in bwd_smem");
+    Barriers &bar = *reinterpret_cast<Barriers *>(smem_raw + kTiles * TB + kFloats * 4);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     const int kt = blockIdx.x % key_tiles, rest = blockIdx.x / key_tiles;
     const int split = rest % a.dkv_splits, set = rest / a.dkv_splits;
     const int bk = set / a.Hk, hk = set % a.Hk;
     const int nk = keys_of(a, bk);
-    const int row_tiles = a.rows_pad / kT;
-    const int i0 = (int)((int64_t)row_tiles * split / a.dkv_splits);
-    const int i1 = (int)((int64_t)row_tiles * (split + 1) / a.dkv_splits);
+    const int i0 = (int)((int64_t)a.tiles * split / a.dkv_splits);
+    const int i1 = (int)((int64_t)a.tiles * (split + 1) / a.dkv_splits);
     // uniform for the CTA: no keys here, or a base that is not aligned
     if (kt * kT >= nk) return;
-    if (smem_u32(sm) & 1023u) {
-        if (threadIdx.x == 0) set_error(g_cross_bwd_err, kErrRange, 0x70);
+    if (sK & 1023u) {
+        if (threadIdx.x == 0) set_error(g_cross_bwd_err, kErrRange, 0x71);
         return;
     }
     if (threadIdx.x == 0) {
-        mbar_init(&bar.k_full, 2);
-        for (int i = 0; i < kRowRing; ++i) {
-            mbar_init(&bar.r_full[i], 2);
-            mbar_init(&bar.r_empty[i], 1);
+        mbar_init(&bar.kv_full, 1);
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(&bar.q_full[i], 1);
+            mbar_init(&bar.q_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.o_full[i], 1);
+            mbar_init(&bar.o_empty[i], 1);
         }
         mbar_init(&bar.s_full, 1);
         mbar_init(&bar.dp_full, 1);
-        mbar_init(&bar.p_full, 8);
+        mbar_init(&bar.dp_read, 8);
         mbar_init(&bar.ds_full, 8);
         mbar_init(&bar.acc_full, 1);
         bar.abort = 0;
@@ -478,129 +609,103 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dkv_kernel(const __grid_
     const uint32_t tmem = bar.tmem_base;
     const Waiter wait{&bar.abort, g_cross_bwd_err};
 
-    if (warp == 9 || warp == 10) {
-        // ------------------------------------------------------------ producers: K, V once, then Q, dO row tiles
-        const int tid = threadIdx.x - 9 * 32;
-        {
-            KeyTile<T, D, 64> tile;
-            tile.load(a.idx ? a.idx + (int64_t)bk * a.M : nullptr, nk, kt, tid);
-            tile.copy(static_cast<const T *>(a.k) + bk * a.kB + hk * a.kH, a.kN, smem_u32(sK), tid);
-            tile.copy(static_cast<const T *>(a.v) + bk * a.vB + hk * a.vH, a.vN, smem_u32(sV), tid);
-            cp_async_commit();
-        }
-        RingFill<kRowRing> ring(bar.r_full, bar.r_empty);
-        const float *nl = a.nlse + (int64_t)set * a.rows_pad, *nd = a.ndelta + (int64_t)set * a.rows_pad;
-        for (int i = i0; i < i1; ++i) {
-            const int r0 = i * kT, nq = min(kT, a.rows - r0), u = i - i0;
-            if (!ring.acquire(wait, 0x60)) break;
-            copy_rows<T, D>(a, bk, hk, r0, nq, kT, static_cast<const T *>(a.q), a.qB, a.qH, a.qN,
-                            smem_u32(sR + ring.slot * TB), tid, 64);
-            if (tid < kT / 4) cp_async16(smem_u32(s_nl + (u % 3) * kT + tid * 4), nl + r0 + tid * 4, true);
-            if (i == i0) {
-                // K and V travel with the first Q tile: announce them together
-                cp_async_commit();
-                cp_async_wait_all();
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.k_full);
+    if (warp == 8) {
+        // ------------------------------------------------------------ K, V
+        if (tma_keys(a, nk, kt)) {
+            if (lane == 0) {
+                mbar_expect_tx(&bar.kv_full, 2 * TB);
+                tma_tile<D>(sK, &m.k, kt * kT, hk, bk, &bar.kv_full);
+                tma_tile<D>(sV, &m.v, kt * kT, hk, bk, &bar.kv_full);
             }
-            ring.issued();
-            if (!ring.acquire(wait, 0x60)) break;
-            copy_rows<T, D>(a, bk, hk, r0, nq, kT, static_cast<const T *>(a.dout), a.dB, a.dH, a.dN,
-                            smem_u32(sR + ring.slot * TB), tid, 64);
-            if (tid < kT / 4) cp_async16(smem_u32(s_nd + (u & 1) * kT + tid * 4), nd + r0 + tid * 4, true);
-            ring.issued();
+        } else {
+            const int32_t *list = a.idx ? a.idx + (int64_t)bk * a.M : nullptr;
+            copy_keys<T, D, 32>(list, nk, kt, static_cast<const T *>(a.k) + bk * a.kB + hk * a.kH, a.kN, sK, lane);
+            copy_keys<T, D, 32>(list, nk, kt, static_cast<const T *>(a.v) + bk * a.vB + hk * a.vH, a.vN, sV, lane);
+            cp_async_commit();
+            cp_async_wait_all();
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.kv_full);
         }
-        ring.flush();
+    } else if (warp == 9 || warp == 10) {
+        // ------------------------------------------------------------ Q rows, dO rows
+        const bool q = warp == 9;
+        const int ns = q ? 3 : 2;
+        uint64_t *full = q ? bar.q_full : bar.o_full, *empty = q ? bar.q_empty : bar.o_empty;
+        float *s_vec = q ? s_nl : s_nd;
+        const float *vec = (q ? a.nlse : a.ndelta) + (int64_t)set * a.tiles * kT;
+        const CUtensorMap *map = q ? &m.q : &m.d;
+        const void *src = q ? a.q : a.dout;
+        const int64_t sB = q ? a.qB : a.dB, sH = q ? a.qH : a.dH, sN = q ? a.qN : a.dN;
+        const uint32_t smem = q ? sQ : sO;
+        bool ok = true;
+        int u = 0;
+        for (int i = i0; i < i1; ++i, ++u) {
+            const int slot = u % ns, use = u / ns;
+            if (use > 0 && !(ok = wait.warp(&empty[slot], (use - 1) & 1, 0x60))) break;
+            // the rows' 128 values first: they are announced together with the tile
+            reinterpret_cast<float4 *>(s_vec + slot * kT)[lane] = reinterpret_cast<const float4 *>(vec + (int64_t)i * kT)[lane];
+            __syncwarp();
+            load_rows<T, D>(a, row_tile<kT>(a, bk, hk, i), hk, 1, map, src, sB, sH, sN, smem + slot * TB, &full[slot]);
+        }
+        if (!ok)
+            for (int i = max(0, u - ns); i < u; ++i) drain(&full[i % ns], (i / ns) & 1);
     } else if (warp == 11) {
         // ------------------------------------------------------------ MMA issuer
         if (lane == 0) {
-            const uint32_t id_s = idesc16<T>(kT, false), id_acc = idesc16<T>(D, true);
-            const uint64_t dK = sw128_desc(smem_u32(sK), 16, 1024), dV = sw128_desc(smem_u32(sV), 16, 1024);
-            const uint64_t dr = sw128_desc(smem_u32(sR), 16, 1024);
-            const uint64_t dmn = sw128_desc(smem_u32(sR), kT * 128, 1024);
-            RingRead<kRowRing> rr;
-            auto product = [&](uint32_t d, uint64_t keys, int slot) {  // d = keys x rows
-                const uint64_t br = dr + (uint64_t)((slot * TB) >> 4);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint64_t o = (uint64_t)(((k >> 2) * (kT * 128) + (k & 3) * 32) >> 4);
-                    mma_ss(d, keys + o, br + o, id_s, k > 0);
-                }
-            };
-            auto accumulate = [&](uint32_t d, uint32_t p, int slot, bool first) {  // d += p x rows
-                const uint64_t b = dmn + (uint64_t)((slot * TB) >> 4);
-#pragma unroll
-                for (int k = 0; k < kT / 16; ++k)
-                    mma_ts(d, p + half_col(k), b + (uint64_t)((k * 2048) >> 4), id_acc, !first || k > 0);
-            };
-            int qs = rr.slot;
-            bool ok = wait(&bar.k_full, 0, 0x61) && wait(&bar.r_full[qs], rr.use & 1, 0x62);
-            int os = 0;
-            if (ok) {
+            RingRead<3> qr;
+            RingRead<2> dr;
+            auto issue_s = [&](int u, int &slot) {
+                slot = qr.slot;
+                if (!wait(&bar.q_full[slot], qr.use & 1, 0x61)) return false;
+                qr.next();
                 tc_fence_after();
-                product(tmem, dK, qs);
+                tile_product<T, D>(tmem + (u & 1) * 128, sK, sQ + slot * TB);
                 mma_commit(&bar.s_full);
-                rr.next();
-                os = rr.slot;
-                ok = wait(&bar.r_full[os], rr.use & 1, 0x63);
-            }
-            if (ok) {
+                return true;
+            };
+            auto issue_dp = [&](int u, int &slot) {
+                slot = dr.slot;
+                if (!wait(&bar.o_full[slot], dr.use & 1, 0x62)) return false;
+                dr.next();
                 tc_fence_after();
-                product(tmem + 128, dV, os);
+                tile_product<T, D>(tmem + ((u & 1) ^ 1) * 128, sV, sO + slot * TB);
                 mma_commit(&bar.dp_full);
-                rr.next();
-            }
-            for (int i = i0; ok && i < i1; ++i) {
-                const int u = i - i0;
-                const bool more = i + 1 < i1;
-                int qn = 0, on = 0;
-                if (!(ok = wait(&bar.p_full, u & 1, 0x64))) break;
+                return true;
+            };
+            int qs = 0, qn = 0, os = 0;
+            bool ok = wait(&bar.kv_full, 0, 0x63) && issue_s(0, qs) && issue_dp(0, os);
+            for (int u = 0; ok && u < i1 - i0; ++u) {
+                const bool more = u + 1 < i1 - i0;
+                if (more && !(ok = wait(&bar.dp_read, u & 1, 0x64) && issue_s(u + 1, qn))) break;
+                if (!(ok = wait(&bar.ds_full, u & 1, 0x65))) break;
                 tc_fence_after();
-                accumulate(tmem + 256, tmem, os, u == 0);
-                mma_commit(&bar.r_empty[os]);
-                if (more) {
-                    qn = rr.slot;
-                    if (!(ok = wait(&bar.r_full[qn], rr.use & 1, 0x65))) break;
-                    rr.next();
-                    tc_fence_after();
-                    product(tmem, dK, qn);
-                    mma_commit(&bar.s_full);
-                }
-                if (!(ok = wait(&bar.ds_full, u & 1, 0x66))) break;
-                tc_fence_after();
-                accumulate(tmem + 384, tmem + 128, qs, u == 0);
-                mma_commit(&bar.r_empty[qs]);
-                if (more) {
-                    on = rr.slot;
-                    if (!(ok = wait(&bar.r_full[on], rr.use & 1, 0x67))) break;
-                    rr.next();
-                    tc_fence_after();
-                    product(tmem + 128, dV, on);
-                    mma_commit(&bar.dp_full);
-                } else {
-                    mma_commit(&bar.acc_full);
-                }
+                const uint32_t p = tmem + (u & 1) * 128;
+                tile_accumulate<T, D>(tmem + 256, p, sO + os * TB, u == 0);
+                mma_commit(&bar.o_empty[os]);
+                tile_accumulate<T, D>(tmem + 384, p + 32, sQ + qs * TB, u == 0);
+                mma_commit(&bar.q_empty[qs]);
+                if (!more) mma_commit(&bar.acc_full);
+                else if (!(ok = issue_dp(u + 1, os))) break;
                 qs = qn;
-                os = on;
             }
         }
         __syncwarp();
-    } else if (warp < 8) {
+    } else {
         // ------------------------------------------------------------ softmax and epilogue
         const int half = warp >> 2, wq = warp & 3, key = wq * 32 + lane;
         const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
-        const uint32_t tS = tmem + lane_off + half * 64, tP = tmem + lane_off + 128 + half * 64;
-        const uint64_t scp = f2pack(a.scale * 1.4426950408889634f, a.scale * 1.4426950408889634f);
+        const uint64_t scp = f2pack(a.scale_log2, a.scale_log2);
         bool ok = true;
-        RingRead<kRowRing> rr;  // nlse, ndelta land with the Q, dO tiles
-        for (int i = i0; i < i1; ++i) {
-            const int u = i - i0;
-            const ulonglong2 *nl = reinterpret_cast<const ulonglong2 *>(s_nl + (u % 3) * kT + half * 64);
-            const ulonglong2 *nd = reinterpret_cast<const ulonglong2 *>(s_nd + (u & 1) * kT + half * 64);
-            if (!(ok = wait.warp(&bar.r_full[rr.slot], rr.use & 1, 0x6b))) break;
-            rr.next();
-            if (!(ok = wait.warp(&bar.s_full, u & 1, 0x68))) break;
+        RingRead<3> qr;  // nlse, ndelta come with the Q, dO tiles
+        RingRead<2> dr;
+        for (int u = 0; u < i1 - i0; ++u) {
+            const ulonglong2 *nl = reinterpret_cast<const ulonglong2 *>(s_nl + qr.slot * kT + half * 64);
+            const ulonglong2 *nd = reinterpret_cast<const ulonglong2 *>(s_nd + dr.slot * kT + half * 64);
+            const uint32_t tS = tmem + lane_off + (u & 1) * 128 + half * 64;
+            const uint32_t tP = tmem + lane_off + ((u & 1) ^ 1) * 128 + half * 64;
+            if (!(ok = wait.warp(&bar.q_full[qr.slot], qr.use & 1, 0x66) && wait.warp(&bar.s_full, u & 1, 0x67))) break;
+            qr.next();
             tc_fence_after();
             uint32_t r[64];
             tmem_ld32(tS, r);
@@ -617,45 +722,33 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dkv_kernel(const __grid_
                 r[4 * c + 2] = __float_as_uint(ex2(x0));
                 r[4 * c + 3] = __float_as_uint(ex2(x1));
             }
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t pk[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    pk[e] = pack2(T(), __uint_as_float(r[c * 32 + 2 * e]), __uint_as_float(r[c * 32 + 2 * e + 1]));
-                tmem_st16(tS + c * 16, pk);
-            }
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.p_full);
-            if (!(ok = wait.warp(&bar.r_full[rr.slot], rr.use & 1, 0x6c))) break;
-            rr.next();
-            if (!(ok = wait.warp(&bar.dp_full, u & 1, 0x69))) break;
+            store_half<T>(tS, r);
+            if (!(ok = wait.warp(&bar.o_full[dr.slot], dr.use & 1, 0x68) && wait.warp(&bar.dp_full, u & 1, 0x69))) break;
+            dr.next();
             tc_fence_after();
             uint32_t d[64];
             tmem_ld32(tP, d);
             tmem_ld32(tP + 32, d + 32);
             tmem_wait_ld();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.dp_read);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t pk[16];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const ulonglong2 n2 = nd[c * 8 + e];
-                    const int q = c * 32 + 4 * e;
-                    float x0, x1;
-                    f2unpack(fmul2(f2pack(__uint_as_float(r[q]), __uint_as_float(r[q + 1])),
-                                   fadd2(f2pack(__uint_as_float(d[q]), __uint_as_float(d[q + 1])), n2.x)),
-                             x0, x1);
-                    pk[2 * e] = pack2(T(), x0, x1);
-                    f2unpack(fmul2(f2pack(__uint_as_float(r[q + 2]), __uint_as_float(r[q + 3])),
-                                   fadd2(f2pack(__uint_as_float(d[q + 2]), __uint_as_float(d[q + 3])), n2.y)),
-                             x0, x1);
-                    pk[2 * e + 1] = pack2(T(), x0, x1);
-                }
-                tmem_st16(tP + c * 16, pk);
+            for (int c = 0; c < 16; ++c) {
+                const ulonglong2 n2 = nd[c];
+                float x0, x1;
+                f2unpack(fmul2(f2pack(__uint_as_float(r[4 * c]), __uint_as_float(r[4 * c + 1])),
+                               fadd2(f2pack(__uint_as_float(d[4 * c]), __uint_as_float(d[4 * c + 1])), n2.x)),
+                         x0, x1);
+                d[4 * c] = __float_as_uint(x0);
+                d[4 * c + 1] = __float_as_uint(x1);
+                f2unpack(fmul2(f2pack(__uint_as_float(r[4 * c + 2]), __uint_as_float(r[4 * c + 3])),
+                               fadd2(f2pack(__uint_as_float(d[4 * c + 2]), __uint_as_float(d[4 * c + 3])), n2.y)),
+                         x0, x1);
+                d[4 * c + 2] = __float_as_uint(x0);
+                d[4 * c + 3] = __float_as_uint(x1);
             }
+            store_half<T>(tS + 32, d);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -663,8 +756,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dkv_kernel(const __grid_
         }
         if (ok && wait.warp(&bar.acc_full, 0, 0x6a)) {
             tc_fence_after();
-            const int m = kt * kT + key;
-            const int64_t at = ((int64_t)split * a.sets + set) * a.M + m;
+            const int key_at = kt * kT + key;
+            const int64_t at = ((int64_t)split * a.sets + set) * a.M + key_at;
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
                 const int col = half * (D / 2) + c * 32;
@@ -672,7 +765,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dkv_kernel(const __grid_
                 float f[32];
                 tmem_ld32(tmem + lane_off + 256 + col, o);
                 tmem_wait_ld();
-                if (m < nk) {
+                if (key_at < nk) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]);
 #pragma unroll
@@ -680,7 +773,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dkv_kernel(const __grid_
                 }
                 tmem_ld32(tmem + lane_off + 384 + col, o);
                 tmem_wait_ld();
-                if (m < nk) {
+                if (key_at < nk) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]) * a.scale;
 #pragma unroll
@@ -693,23 +786,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1) cross_dkv_kernel(const __grid_
 }
 
 // dk, dv of every key: the row ranges' parts added in order; keys that no row
-// may read get zeros.
-struct DkvOut {
-    void *dk, *dv;
-    int64_t ks[3], vs[3];  // element strides of batch, head, key
-    const int32_t *inv;    // place of a key in its list or -1, or null
-};
-
+// may read get zeros.  inv: a key's place in its list or -1, or null.
 template <typename T>
 __global__ void __launch_bounds__(256) cross_dkv_join_kernel(const __grid_constant__ CrossArgs a,
-                                                             const __grid_constant__ DkvOut out, int D)
+                                                             const int32_t *inv, int D)
 {
     const int lpr = D / 8;
     const int64_t row = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / lpr;  // set * M + m
     const int c8 = threadIdx.x % lpr;
     if (row >= (int64_t)a.sets * a.M) return;
     const int set = (int)(row / a.M), m = (int)(row % a.M), bk = set / a.Hk, hk = set % a.Hk;
-    const int place = out.inv ? out.inv[(int64_t)bk * a.M + m] : (m < keys_of(a, bk) ? m : -1);
+    const int place = inv ? inv[(int64_t)bk * a.M + m] : (m < keys_of(a, bk) ? m : -1);
     float sk[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, sv[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (place >= 0) {
 #pragma unroll 2
@@ -725,17 +812,17 @@ __global__ void __launch_bounds__(256) cross_dkv_join_kernel(const __grid_consta
             }
         }
     }
-    store8(static_cast<T *>(out.dk) + bk * out.ks[0] + hk * out.ks[1] + m * out.ks[2] + c8 * 8, sk);
-    store8(static_cast<T *>(out.dv) + bk * out.vs[0] + hk * out.vs[1] + m * out.vs[2] + c8 * 8, sv);
+    store8(static_cast<T *>(a.dk) + bk * a.dkB + hk * a.dkH + m * a.dkN + c8 * 8, sk);
+    store8(static_cast<T *>(a.dv) + bk * a.dvB + hk * a.dvH + m * a.dvN + c8 * 8, sv);
 }
 
 template <typename T, int D>
 static cudaError_t bwd_attr()
 {
     const cudaError_t e = cudaFuncSetAttribute(cross_dq_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)dq_smem(D));
+                                               (int)bwd_smem(D));
     if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(cross_dkv_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dkv_smem(D));
+    return cudaFuncSetAttribute(cross_dkv_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bwd_smem(D));
 }
 
 cudaError_t cross_bwd_configure()
@@ -773,35 +860,34 @@ static int best_split(int64_t items, int64_t len, int sms, double fixed, double 
     return best;
 }
 
-int cross_dq_splits(int64_t sets, int64_t rows, int64_t M, int64_t rows_total, int D, int sms)
+int cross_dq_splits(int64_t sets, int64_t tiles, int64_t M, int64_t rows_total, int D, int sms)
 {
-    const int64_t items = sets * ((rows + kT - 1) / kT), len = (M + kT - 1) / kT;
+    const int64_t items = sets * tiles, len = (M + kT - 1) / kT;
     if (items >= sms) return 1;  // persistent: items even out by themselves
-    return best_split(items, len, sms, 2.0, (double)rows_total * D * 8.0 / 6e6, 3.0);
+    return best_split(items, len, sms, 2.0, (double)rows_total * D * 16.0 / 6e6, 3.0);
 }
 
-int cross_dkv_splits(int64_t sets, int64_t rows, int64_t M, int D, int sms)
+int cross_dkv_splits(int64_t sets, int64_t tiles, int64_t M, int D, int sms)
 {
-    const int64_t items = sets * ((M + kT - 1) / kT), len = (rows + kT - 1) / kT;
+    const int64_t items = sets * ((M + kT - 1) / kT), len = tiles;
     return best_split(items, len, sms, 4.0, (double)(sets * M) * D * 16.0 / 6e6, 0.0);
 }
 
 template <typename T, int D>
-static void launch_bwd_t(const CrossArgs &a, int sms, const DkvOut &out, cudaStream_t st)
+static void launch_bwd_t(const CrossArgs &a, const CrossMaps &m, int sms, const int32_t *inv, cudaStream_t st)
 {
     const int64_t key_threads = (int64_t)a.sets * a.M * (D / 8);
     const unsigned join_blocks = (unsigned)((key_threads + 255) / 256);
     if (a.N == 0) {  // no row: dk = dv = 0
         CrossArgs none = a;
         none.dkv_splits = 0;
-        cross_dkv_join_kernel<T><<<join_blocks, 256, 0, st>>>(none, out, D);
+        cross_dkv_join_kernel<T><<<join_blocks, 256, 0, st>>>(none, inv, D);
         count_launches(1);
         return;
     }
-    const int64_t row_threads = (int64_t)a.sets * a.rows_pad * (D / 8);
-    cross_rows_kernel<T><<<(unsigned)((row_threads + 255) / 256), 256, 0, st>>>(a, D);
-    const int dq_items = a.sets * a.dq_splits * (a.rows_pad / kT);
-    cross_dq_kernel<T, D><<<dq_items < sms ? dq_items : sms, kBwdThreads, dq_smem(D), st>>>(a, dq_items);
+    cross_rows_kernel<T, D><<<(unsigned)(a.sets * a.tiles), 256, 0, st>>>(a);
+    const int dq_items = a.sets * a.dq_splits * a.tiles;
+    cross_dq_kernel<T, D><<<dq_items < sms ? dq_items : sms, kBwdThreads, bwd_smem(D), st>>>(a, m, dq_items);
     count_launches(2);
     if (a.dq_splits > 1) {
         const int64_t threads = (int64_t)a.B * a.H * a.N * (D / 8);
@@ -810,21 +896,20 @@ static void launch_bwd_t(const CrossArgs &a, int sms, const DkvOut &out, cudaStr
     }
     if (a.M == 0) return;
     const int key_tiles = (a.M + kT - 1) / kT;
-    cross_dkv_kernel<T, D><<<(unsigned)(a.sets * a.dkv_splits * key_tiles), kBwdThreads, dkv_smem(D), st>>>(a, key_tiles);
-    cross_dkv_join_kernel<T><<<join_blocks, 256, 0, st>>>(a, out, D);
+    cross_dkv_kernel<T, D><<<(unsigned)(a.sets * a.dkv_splits * key_tiles), kBwdThreads, bwd_smem(D), st>>>(a, m, key_tiles);
+    cross_dkv_join_kernel<T><<<join_blocks, 256, 0, st>>>(a, inv, D);
     count_launches(2);
 }
 
-void launch_cross_bwd(const CrossArgs &a, int D, bool f16, int sms, const int32_t *inv, void *dk, const int64_t *dks,
-                      void *dv, const int64_t *dvs, cudaStream_t st)
+void launch_cross_bwd(const CrossArgs &a, const CrossMaps &m, int D, bool f16, int sms, const int32_t *inv,
+                      cudaStream_t st)
 {
-    DkvOut out{dk, dv, {dks[0], dks[1], dks[2]}, {dvs[0], dvs[1], dvs[2]}, inv};
     if (f16) {
-        if (D == 128) launch_bwd_t<__half, 128>(a, sms, out, st);
-        else launch_bwd_t<__half, 64>(a, sms, out, st);
+        if (D == 128) launch_bwd_t<__half, 128>(a, m, sms, inv, st);
+        else launch_bwd_t<__half, 64>(a, m, sms, inv, st);
     } else {
-        if (D == 128) launch_bwd_t<__nv_bfloat16, 128>(a, sms, out, st);
-        else launch_bwd_t<__nv_bfloat16, 64>(a, sms, out, st);
+        if (D == 128) launch_bwd_t<__nv_bfloat16, 128>(a, m, sms, inv, st);
+        else launch_bwd_t<__nv_bfloat16, 64>(a, m, sms, inv, st);
     }
 }
 

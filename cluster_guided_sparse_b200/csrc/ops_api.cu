@@ -320,10 +320,15 @@ op::CrossArgs cross_sizes(const scope_tensor *q, const scope_tensor *k)
     op::CrossArgs a{};
     a.B = (int)q->B; a.Bk = (int)k->B; a.H = (int)q->H; a.Hk = (int)k->H; a.N = (int)q->N; a.M = (int)k->N;
     a.G = a.H / a.Hk;
-    a.GN = a.G * a.N;
-    a.rows = a.Bk == a.B ? a.GN : a.B * a.GN;
+    a.heads = a.Bk == a.B ? a.G : a.B * a.G;
     a.sets = a.Bk * a.Hk;
-    a.row_tiles = (a.rows + 255) / 256;
+    // Tiles by head waste up to 127 rows a head, folded ones cost copies by
+    // threads instead of TMA.
+    const int padded = (a.N + 127) / 128 * 128;
+    a.fold = a.heads > 1 && padded > 1.25 * a.N;
+    const int rows = a.heads * a.N;
+    a.pairs = a.fold ? (rows + 255) / 256 : a.heads * ((a.N + 255) / 256);
+    a.tiles = a.fold ? (rows + 127) / 128 : a.heads * (padded / 128);
     return a;
 }
 
@@ -331,8 +336,8 @@ CrossLayout cross_layout(op::CrossArgs &a, int D, bool masked)
 {
     CrossLayout L{};
     const int64_t total = (int64_t)a.B * a.H * a.N;
-    a.splits = op::cross_fwd_splits(a.sets, a.row_tiles, a.M, total, D, kSms);
-    a.items = a.sets * a.splits * a.row_tiles;
+    a.splits = op::cross_fwd_splits(a.sets, a.pairs, a.M, total, D, kSms);
+    a.items = a.sets * a.splits * a.pairs;
     size_t cur = 256;
     L.idx = take(cur, masked ? (size_t)a.Bk * a.M * 4 : 0);
     L.cnt = take(cur, masked ? (size_t)a.Bk * 4 : 0);
@@ -343,24 +348,26 @@ CrossLayout cross_layout(op::CrossArgs &a, int D, bool masked)
 }
 
 struct CrossBwdLayout {
-    size_t idx, cnt, inv, nlse, ndelta, part_dq, part_dk, part_dv, total;
+    size_t idx, cnt, inv, nlse, ndelta, part_t, part_e, part_delta, part_dk, part_dv, total;
 };
 
 CrossBwdLayout cross_bwd_layout(op::CrossArgs &a, int D, bool masked)
 {
     CrossBwdLayout L{};
     const int64_t total = (int64_t)a.B * a.H * a.N;
-    a.rows_pad = (a.rows + 127) / 128 * 128;
-    a.dq_splits = op::cross_dq_splits(a.sets, a.rows, a.M, total, D, kSms);
-    a.dkv_splits = op::cross_dkv_splits(a.sets, a.rows, a.M, D, kSms);
+    a.dq_splits = op::cross_dq_splits(a.sets, a.tiles, a.M, total, D, kSms);
+    a.dkv_splits = op::cross_dkv_splits(a.sets, a.tiles, a.M, D, kSms);
     size_t cur = 256;
-    const size_t keys = masked ? (size_t)a.Bk * a.M * 4 : 0, rows = (size_t)a.sets * a.rows_pad * 4;
+    const size_t keys = masked ? (size_t)a.Bk * a.M * 4 : 0, rows = (size_t)a.sets * a.tiles * 128 * 4;
     L.idx = take(cur, keys);
     L.inv = take(cur, keys);
     L.cnt = take(cur, masked ? (size_t)a.Bk * 4 : 0);
     L.nlse = take(cur, rows);
     L.ndelta = take(cur, rows);
-    L.part_dq = take(cur, a.dq_splits > 1 ? (size_t)a.dq_splits * total * D * 4 : 0);
+    const size_t rows_split = a.dq_splits > 1 ? (size_t)a.dq_splits * total * 4 : 0;
+    L.part_t = take(cur, rows_split * D);
+    L.part_e = take(cur, rows_split * D);
+    L.part_delta = take(cur, rows_split);
     const size_t parts = (size_t)a.dkv_splits * a.sets * a.M * D * 4;
     L.part_dk = take(cur, parts);
     L.part_dv = take(cur, parts);
@@ -380,6 +387,46 @@ void cross_tensors(op::CrossArgs &a, const scope_tensor *q, const scope_tensor *
     a.kv_len = keys ? keys->len : nullptr;
     a.scale = scale != 0.f ? scale : 1.f / std::sqrt((float)q->D);
     a.scale_log2 = a.scale * 1.4426950408889634f;
+}
+
+// Tensor map of 128-row x 64-column boxes; false where TMA cannot address the
+// layout (a stride of 2^40 bytes or more).
+bool tile_map(CUtensorMap *m, const scope_tensor *t)
+{
+    using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static std::atomic<Encode> found{nullptr};
+    Encode encode = found;
+    if (!encode) {
+        void *fn = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess || !fn)
+            return false;
+        found = encode = (Encode)fn;
+    }
+    const RowStrides s = op::strides_of(t);
+    // a dimension of one entry may have any stride
+    const int64_t ext[3] = {t->N, t->H, t->B}, str[3] = {s.sN, s.sH, s.sB};
+    cuuint64_t dims[4] = {(cuuint64_t)t->D}, strides[3];
+    for (int i = 0; i < 3; ++i) {
+        dims[i + 1] = (cuuint64_t)ext[i];
+        strides[i] = (cuuint64_t)(ext[i] > 1 ? str[i] : t->D) * 2;
+        if (strides[i] >= (cuuint64_t)1 << 40) return false;
+    }
+    const cuuint32_t box[4] = {64, 128, 1, 1}, one[4] = {1, 1, 1, 1};
+    return encode(m, t->dtype == SCOPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, t->ptr,
+                  dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The maps that a call's kernels use; what has none is copied by threads.
+void cross_maps(op::CrossArgs &a, op::CrossMaps &m, const scope_tensor *q, const scope_tensor *k, const scope_tensor *v,
+                const scope_tensor *d)
+{
+    a.tma_kv = a.M > 0 && !a.idx && tile_map(&m.k, k) && tile_map(&m.v, v);
+    a.tma_rows = !a.fold && a.N > 0 && tile_map(&m.q, q) && (!d || tile_map(&m.d, d));
 }
 
 }  // namespace
@@ -419,7 +466,9 @@ extern "C" scope_status scope_cross_attn(const scope_tensor *q, const scope_tens
         a.idx = idx;
         a.cnt = cnt;
     }
-    op::launch_cross_fwd(a, (int)q->D, q->dtype == SCOPE_F16, kSms, s);
+    op::CrossMaps m;
+    cross_maps(a, m, q, k, v, nullptr);
+    op::launch_cross_fwd(a, m, (int)q->D, q->dtype == SCOPE_F16, kSms, s);
     return launch_status("scope_cross_attn");
 }
 
@@ -462,7 +511,9 @@ extern "C" scope_status scope_cross_attn_backward(const scope_tensor *d_o, const
     char *ws = (char *)workspace;
     a.nlse = (float *)(ws + L.nlse);
     a.ndelta = (float *)(ws + L.ndelta);
-    a.part_dq = (float *)(ws + L.part_dq);
+    a.part_t = (float *)(ws + L.part_t);
+    a.part_e = (float *)(ws + L.part_e);
+    a.part_delta = (float *)(ws + L.part_delta);
     a.part_dk = (float *)(ws + L.part_dk);
     a.part_dv = (float *)(ws + L.part_dv);
     cudaStream_t s = (cudaStream_t)stream;
@@ -474,8 +525,13 @@ extern "C" scope_status scope_cross_attn_backward(const scope_tensor *d_o, const
         a.idx = idx;
         a.cnt = cnt;
     }
-    const int64_t dks[3] = {ks.sB, ks.sH, ks.sN}, dvs[3] = {vs.sB, vs.sH, vs.sN};
-    op::launch_cross_bwd(a, (int)q->D, q->dtype == SCOPE_F16, kSms, inv, dk->ptr, dks, dv->ptr, dvs, s);
+    a.dk = dk->ptr;
+    a.dkB = ks.sB; a.dkH = ks.sH; a.dkN = ks.sN;
+    a.dv = dv->ptr;
+    a.dvB = vs.sB; a.dvH = vs.sH; a.dvN = vs.sN;
+    op::CrossMaps m;
+    cross_maps(a, m, q, k, v, d_o);
+    op::launch_cross_bwd(a, m, (int)q->D, q->dtype == SCOPE_F16, kSms, inv, s);
     return launch_status("scope_cross_attn_backward");
 }
 
