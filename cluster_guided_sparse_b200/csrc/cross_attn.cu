@@ -5,25 +5,28 @@
 //   o_i = sum_j e^(s_ij - lse_i) v_j;  a row without keys gets o = 0, lse = -inf.
 //
 // Bound: 4 D flops a (row, key) pair on the tensor cores against one
-// exponential a pair (16 a clock and SM): at D = 128 both take 1024 clocks a
-// 128 x 128 tile, so the two must overlap; below some 300 keys the rows' own
-// bytes (q in, o out) take longer than either and HBM is the bound.
+// exponential a pair (16 a clock and SM), both 1024 clocks a 128 x 128 tile at
+// D = 128; but S with operands in shared memory reads that at its full rate, so
+// with the copies into it shared memory is the first limit (1280 clocks).  Below
+// some 300 keys the rows' own bytes (q in, o out) take longer and HBM is the bound.
 //
 // One persistent CTA per SM walks work items = (key set, key range, 256
 // rows).  The two 128-row tiles of an item share every K/V tile, which halves
-// the L2 traffic, and are in opposite phases: one's softmax runs under the
-// other's products.  K and V tiles of 128 keys go through one ring of
-// shared-memory stages; the next item's Q rows land in a second buffer while
-// this item runs, and an item's epilogue overlaps the next item's first
-// products.
+// the L2 traffic.  The keys go in tiles of 64 with two S buffers a row tile, so
+// the products of the tile after next are out while the softmax works on this
+// one: neither waits for the other's latency (one buffer of 128 keys took 4200
+// clocks a row tile and 128 keys, of which the products are 1024).  The steps run on
+// over item borders: the next item's first S tiles are there before this one's
+// epilogue.  Q rows have two buffers for the same reason.
 //
-// Warp roles (384 threads):
-//   warps 0-3, 4-7  softmax and epilogue of tile 0, 1 (one thread per row); O
-//                   leaves through the item's Q buffer as whole row segments
-//   warp 8          Q rows     } by TMA, or cp.async where a tile's rows are not
-//   warps 9-10      K, V rows  } in order (cross_common.cuh)
-//   warp 11         tcgen05.mma issuer (one lane), owns the TMEM allocation
-// TMEM (512 columns): S0 [0,128) S1 [128,256) O0 [256,256+D) O1 [384,384+D);
+// Warp roles (416 threads):
+//   warps 0-3, 4-7  softmax and epilogue of row tile 0, 1 (one thread per row)
+//   warps 8, 9, 10  Q, K, V rows by TMA, or cp.async where a tile's rows are not
+//                   in order (cross_common.cuh)
+//   warps 11, 12    tcgen05.mma issuers of row tile 0, 1; warp 11 owns the TMEM
+//                   allocation.  (One issuer for both was the limit: its waits,
+//                   commits and issues came to 3200 clocks for 1280 of products.)
+// TMEM, of each row tile's 256 columns: S0 [0,64) S1 [64,128) O [128,128+D);
 // P (16 bit) overwrites its S.  The softmax runs in base 2 with a lazy
 // rescale: O and l move to a new maximum only when it grew by more than 2^8,
 // so P stays below 2^8.  P is rounded to the inputs' type for the product
@@ -46,60 +49,91 @@ using namespace tc;
 
 static __device__ int32_t g_cross_err[4];
 
-constexpr int kFwdThreads = 384;
-constexpr int kTile = 128;  // rows of a Q tile, keys of a K/V tile
+constexpr int kFwdThreads = 416;
+constexpr int kTile = 128;  // rows of a Q tile
 
-constexpr int fwd_stages(int D) { return D == 128 ? 3 : 4; }
-constexpr size_t fwd_smem(int D) { return (size_t)(4 + fwd_stages(D)) * kTile * D * 2 + 1024; }
+constexpr int fwd_stages(int D) { return D == 128 ? 3 : 6; }  // of K and of V
+constexpr size_t fwd_smem(int D) { return (size_t)(4 * kTile + 2 * fwd_stages(D) * kFwdKeys) * D * 2 + 1024; }
 
 struct FwdItem {
     int bk, hk, t0, t1, nk, split;
     RowTile r;
 };
 
-__device__ __forceinline__ FwdItem fwd_item(const CrossArgs &a, int item)
+__device__ __noinline__ FwdItem fwd_item(const CrossArgs &a, int item)
 {
     FwdItem w;
-    const int rt = item % a.pairs, rest = item / a.pairs;
-    w.split = rest % a.splits;
-    const int set = rest / a.splits;
-    w.bk = set / a.Hk;
-    w.hk = set % a.Hk;
+    int rt, set;
+    item = min(item, a.items - 1);  // behind the last one any
+    set = a.by_splits(a.by_tiles(item, rt), w.split);
+    w.bk = a.by_Hk(set, w.hk);
     w.r = row_tile<2 * kTile>(a, w.bk, w.hk, rt);
     w.nk = keys_of(a, w.bk);
-    const int tiles = (w.nk + kTile - 1) / kTile;
-    w.t0 = (int)((int64_t)tiles * w.split / a.splits);
-    w.t1 = (int)((int64_t)tiles * (w.split + 1) / a.splits);
+    split_range((w.nk + kFwdKeys - 1) / kFwdKeys, w.split, a.by_splits, w.t0, w.t1);
     return w;
 }
+
+// A CTA's key tiles in order, over its items; by a whole warp.
+struct FwdSteps {
+    int item, j, t1, nt;  // nt: row tiles of the item
+    int seq = -1;         // items begun before this one
+    bool first;           // of its item
+    __device__ __forceinline__ bool seek(const CrossArgs &a, int from)
+    {
+#pragma unroll 1
+        for (item = from; item < a.items; item += gridDim.x) {
+            const FwdItem w = fwd_item(a, item);
+            j = uniform(w.t0);
+            t1 = uniform(w.t1);
+            if (j == t1) continue;
+            nt = uniform(w.r.nq) > kTile ? 2 : 1;
+            first = true;
+            ++seq;
+            return true;
+        }
+        return false;
+    }
+    __device__ __forceinline__ bool next(const CrossArgs &a)
+    {
+        first = false;
+        return ++j < t1 || seek(a, item + gridDim.x);
+    }
+};
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_constant__ CrossArgs a, const __grid_constant__ CrossMaps m)
 {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = (unsigned char *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    constexpr int TB = kTile * D * 2;  // bytes of a tile
+    constexpr int TB = kTile * D * 2, KB = kFwdKeys * D * 2;  // bytes of a row tile, of a key tile
     constexpr int NS = fwd_stages(D);
-    unsigned char *sQ = sm;            // 2 buffers of 2 tiles
-    unsigned char *sKV = sm + 4 * TB;  // NS stages
+    const uint32_t sQ = smem_u32(sm);  // 2 buffers of 2 tiles
+    const uint32_t sK = sQ + 4 * TB, sV = sK + NS * KB;
 
-    __shared__ uint64_t q_full[2], q_empty[2], kv_full[NS], kv_empty[NS], s_full[2], p_full[2], o_full[2], o_empty[2];
+    __shared__ uint64_t q_full[2], q_empty[2], k_full[NS], k_empty[NS], v_full[NS], v_empty[NS];
+    // Of each row tile.  Steps alternate between two barriers each: with one, S being two steps ahead, a waiter
+    // could find the phase after next, which looks like the phase before.
+    __shared__ uint64_t s_full[2][2], p_full[2][2], o_full[2][2], o_empty[2];
     __shared__ uint32_t tmem_base_sh;
     __shared__ int abort_sh;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
-            mbar_init(&q_empty[i], 8);
-            mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 4);
-            mbar_init(&o_full[i], 1);
+            mbar_init(&q_empty[i], 2);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&s_full[i][b], 1);
+                mbar_init(&p_full[i][b], 4);
+                mbar_init(&o_full[i][b], 1);
+            }
             mbar_init(&o_empty[i], 4);
         }
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&kv_full[i], 2);
-            mbar_init(&kv_empty[i], 1);
+            mbar_init(&k_full[i], 1);
+            mbar_init(&k_empty[i], 2);
+            mbar_init(&v_full[i], 1);
+            mbar_init(&v_empty[i], 2);
         }
         abort_sh = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -111,274 +145,234 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_base_sh;
+    const uint32_t tmem = uniform(tmem_base_sh);
     const Waiter wait{&abort_sh, g_cross_err};
 
     if (warp == 8) {
         // ------------------------------------------------------------ Q rows
         int qi = 0;
         bool ok = true;
+#pragma unroll 1
         for (int item = blockIdx.x; item < a.items; item += gridDim.x) {
             const FwdItem w = fwd_item(a, item);
             if (w.t0 == w.t1) continue;
             const int buf = qi & 1;
             if (qi >= 2 && !(ok = wait.warp(&q_empty[buf], ((qi >> 1) - 1) & 1, 0x40))) break;
-            load_rows<T, D>(a, w.r, w.hk, w.r.nq > kTile ? 2 : 1, &m.q, a.q, a.qB, a.qH, a.qN,
-                            smem_u32(sQ + buf * 2 * TB), &q_full[buf]);
+            load_rows<T, D>(a, w.r, w.hk, w.r.nq > kTile ? 2 : 1, &m.q, a.q, a.qB, a.qH, a.qN, sQ + buf * 2 * TB,
+                            &q_full[buf]);
             ++qi;
         }
         if (!ok)
-            for (int i = qi - 2; i < qi; ++i) drain(&q_full[i & 1], (i >> 1) & 1);
+            for (int i = max(0, qi - 2); i < qi; ++i) drain(&q_full[i & 1], (i >> 1) & 1);
     } else if (warp == 9 || warp == 10) {
-        // ------------------------------------------------------------ K, V rows
-        const int tid = threadIdx.x - 9 * 32;
-        RingFill<NS> ring(kv_full, kv_empty);
-        bool ok = true;
-        for (int item = blockIdx.x; ok && item < a.items; item += gridDim.x) {
-            const FwdItem w = fwd_item(a, item);
-            const T *k = static_cast<const T *>(a.k) + w.bk * a.kB + w.hk * a.kH;
-            const T *v = static_cast<const T *>(a.v) + w.bk * a.vB + w.hk * a.vH;
-            const int32_t *list = a.idx ? a.idx + (int64_t)w.bk * a.M : nullptr;
-            for (int j = w.t0; ok && j < w.t1; ++j) {
-                const bool whole = tma_keys(a, w.nk, j);
+        // ------------------------------------------------------------ K rows, V rows
+        auto decode = [&](int item) { return fwd_item(a, item); };
+        if (warp == 9)
+            fill_keys<T, D, kFwdKeys>(a, RingFill<NS>(k_full, k_empty), &m.k, a.k, a.kB, a.kH, a.kN, sK, a.items, wait,
+                                      0x41, decode);
+        else
+            fill_keys<T, D, kFwdKeys>(a, RingFill<NS>(v_full, v_empty), &m.v, a.v, a.vB, a.vH, a.vN, sV, a.items, wait,
+                                      0x42, decode);
+    } else if (warp >= 11) {
+        // ------------------------------------------------------------ MMA issuer of row tile t
+        // The whole warp runs the steps, so their values are uniform, and one lane issues (where a single lane ran
+        // them, each operand of an instruction cost a search for the lanes that share it: 1.3 times the call's time)
+        const int t = warp - 11;
+        const uint32_t id_qk = idesc16<T>(kFwdKeys, false), id_pv = idesc16<T>(D, true);
+        const uint64_t dq = sw128_desc(sQ + t * TB, 16, 1024), dk = sw128_desc(sK, 16, 1024);
+        const uint64_t dv = sw128_desc(sV, kFwdKeys * 128, 1024);
+        const uint32_t tS = tmem + t * 256, tO = tS + 128;
+        FwdSteps front, back;  // steps whose S, whose PV is next; the front is two ahead
+        RingRead<NS> kr, vr;
+        int ns = 0, np = 0, no = 0;  // of this row tile: S, PV issued, items done
+        bool ok = true, more = front.seek(a, blockIdx.x), work = more;
+        back = front;
+        int lead = 0;
 #pragma unroll 1
-                for (int x = 0; x < 2; ++x) {
-                    if (!(ok = ring.acquire(wait, 0x41))) break;
-                    const uint32_t dst = smem_u32(sKV + ring.slot * TB);
-                    if (whole) {
-                        ring.template tma<D>(warp == 9, dst, x ? &m.v : &m.k, j * kTile, w.hk, w.bk);
-                    } else {
-                        copy_keys<T, D, 64>(list, w.nk, j, x ? v : k, x ? a.vN : a.kN, dst, tid);
-                        ring.issued();
+        while (ok && work) {
+            const bool pv = lead == 2 || !more;
+            if (pv) {  // O (+)= P V of the back step
+                uint64_t *v = &v_full[vr.slot];
+                if (t < back.nt) {
+                    const int b = np & 1;
+                    if (!(ok = wait.all(&p_full[t][b], (np >> 1) & 1, 0x45, v, vr.use & 1, 0x47))) break;
+                    // the previous item's epilogue has read O
+                    if (back.first && no > 0 && !(ok = wait.warp(&o_empty[t], (no - 1) & 1, 0x46))) break;
+                    tc_fence_after();
+                    const uint64_t bv = dv + (uint64_t)((vr.slot * KB) >> 4);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < kFwdKeys / 16; ++k)
+                            mma_ts(tO, tS + b * 64 + k * 8, bv + (uint64_t)((k * 2048) >> 4), id_pv, !back.first || k > 0);
+                        mma_commit(&o_full[t][b]);
+                        mma_commit(&v_empty[vr.slot]);
                     }
+                    __syncwarp();
+                    ++np;
+                    if (back.j + 1 == back.t1) ++no;
+                } else {
+                    if (!(ok = wait.warp(v, vr.use & 1, 0x4f))) break;
+                    if (lane == 0) mbar_arrive(&v_empty[vr.slot]);
                 }
+                vr.next();
+                work = back.next(a);
+            } else {
+                ++lead;
+            }
+            if (more) {  // S = Q K^T of the front step
+                const int buf = front.seq & 1;
+                const bool last = front.j + 1 == front.t1;
+                if (!(ok = wait.all(&k_full[kr.slot], kr.use & 1, 0x44, &q_full[buf], (front.seq >> 1) & 1, 0x43))) break;
+                if (t < front.nt) {
+                    tc_fence_after();
+                    const uint64_t aq = dq + (uint64_t)((buf * 2 * TB) >> 4), bk = dk + (uint64_t)((kr.slot * KB) >> 4);
+                    const int b = ns & 1;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k)
+                            mma_ss(tS + b * 64, aq + (uint64_t)(((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4),
+                                   bk + (uint64_t)(((k >> 2) * (kFwdKeys * 128) + (k & 3) * 32) >> 4), id_qk, k > 0);
+                        mma_commit(&s_full[t][b]);
+                        mma_commit(&k_empty[kr.slot]);
+                        if (last) mma_commit(&q_empty[buf]);
+                    }
+                    __syncwarp();
+                    ++ns;
+                } else if (lane == 0) {
+                    mbar_arrive(&k_empty[kr.slot]);
+                    if (last) mbar_arrive(&q_empty[buf]);
+                }
+                kr.next();
+                more = front.next(a);
             }
         }
-        ring.finish(!ok);
-    } else if (warp == 11) {
-        // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            const uint32_t id_qk = idesc16<T>(kTile, false), id_pv = idesc16<T>(D, true);
-            const uint64_t dq = sw128_desc(smem_u32(sQ), 16, 1024);
-            const uint64_t dk = sw128_desc(smem_u32(sKV), 16, 1024);
-            const uint64_t dv = sw128_desc(smem_u32(sKV), kTile * 128, 1024);
-            int qi = 0, np[2] = {0, 0}, no[2] = {0, 0};
-            RingRead<NS> kv;
-            bool ok = true;
-            for (int item = blockIdx.x; ok && item < a.items; item += gridDim.x) {
-                const FwdItem w = fwd_item(a, item);
-                if (w.t0 == w.t1) continue;
-                const int nt = w.r.nq > kTile ? 2 : 1, buf = qi & 1;
-                // S_t = Q_t K^T
-                auto issue_qk = [&](int t, int ks) {
-                    const uint64_t aq = dq + (uint64_t)(((buf * 2 + t) * TB) >> 4);
-                    const uint64_t bk = dk + (uint64_t)((ks * TB) >> 4);
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint64_t o = (uint64_t)(((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4);
-                        mma_ss(tmem + t * 128, aq + o, bk + o, id_qk, k > 0);
-                    }
-                    mma_commit(&s_full[t]);
-                    if (t == nt - 1) mma_commit(&kv_empty[ks]);
-                };
-                ok = wait(&q_full[buf], (qi >> 1) & 1, 0x42) && wait(&kv_full[kv.slot], kv.use & 1, 0x43);
-                if (!ok) break;
-                tc_fence_after();
-                for (int t = 0; t < nt; ++t) issue_qk(t, kv.slot);
-                kv.next();
-                for (int j = w.t0; ok && j < w.t1; ++j) {
-                    const int vs = kv.slot;
-                    if (!(ok = wait(&kv_full[vs], kv.use & 1, 0x44))) break;
-                    kv.next();
-                    const bool more = j + 1 < w.t1;
-                    for (int t = 0; t < nt; ++t) {
-                        if (!(ok = wait(&p_full[t], np[t] & 1, 0x45))) break;
-                        ++np[t];
-                        // the previous item's epilogue has read O_t
-                        if (j == w.t0 && no[t] > 0 && !(ok = wait(&o_empty[t], (no[t] - 1) & 1, 0x46))) break;
-                        tc_fence_after();
-                        const uint64_t bv = dv + (uint64_t)((vs * TB) >> 4);
-#pragma unroll
-                        for (int k = 0; k < kTile / 16; ++k)
-                            mma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, bv + (uint64_t)((k * 2048) >> 4), id_pv,
-                                   j > w.t0 || k > 0);
-                        if (t == nt - 1) mma_commit(&kv_empty[vs]);
-                        if (more) {
-                            if (t == 0 && !(ok = wait(&kv_full[kv.slot], kv.use & 1, 0x47))) break;
-                            tc_fence_after();
-                            issue_qk(t, kv.slot);
-                        } else {
-                            mma_commit(&o_full[t]);
-                            ++no[t];
-                        }
-                    }
-                    if (more) kv.next();
-                }
-                ++qi;
-            }
-        }
-        __syncwarp();
-    } else if (warp < 8) {
+    } else {
         // ------------------------------------------------------------ softmax and epilogue
-        const int t = warp >> 2, wq = warp & 3, row = wq * 32 + lane;
-        const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
-        const uint32_t tS = tmem + lane_off + t * 128, tO = tmem + lane_off + 256 + t * 128;
-        int ns = 0, no = 0, qi = 0;
+        const int t = warp >> 2, wq = warp & 3;
+        const uint32_t tT = tmem + ((uint32_t)(wq * 32) << 16) + t * 256, tO = tT + 128;
+        const uint64_t scp = f2pack(a.scale_log2, a.scale_log2);
+        int ns = 0;
         bool ok = true;
+        FwdItem w = fwd_item(a, blockIdx.x);
+#pragma unroll 1
         for (int item = blockIdx.x; ok && item < a.items; item += gridDim.x) {
-            const FwdItem w = fwd_item(a, item);
-            const bool some = w.t0 < w.t1;  // uniform for the CTA
-            const int buf = qi & 1;
-            if (some) ++qi;
-            if (w.r.nq <= t * kTile) {
-                // no rows here: the item's Q is free as far as this tile goes (but not before it has come)
-                if (some) {
-                    if (!(ok = wait.warp(&q_full[buf], ((qi - 1) >> 1) & 1, 0x4c))) break;
-                    if (lane == 0) mbar_arrive(&q_empty[buf]);
-                }
+            if (w.r.nq <= t * kTile) {  // no rows here
+                w = fwd_item(a, item + gridDim.x);
                 continue;
             }
-            float m_run = -INFINITY, l = 0.f;
-            for (int j = w.t0; j < w.t1; ++j) {
-                if (!(ok = wait.warp(&s_full[t], ns & 1, 0x48 + t))) break;
-                ++ns;
+            const bool some = w.t0 < w.t1;
+            float m_run = -INFINITY;
+            uint64_t lA = 0ull, lB = 0ull;
+#pragma unroll 1
+            for (int j = w.t0; j < w.t1; ++j, ++ns) {
+                const uint32_t tS = tT + (ns & 1) * 64;
+                if (!(ok = wait.warp(&s_full[t][ns & 1], (ns >> 1) & 1, 0x48 + t))) break;
                 tc_fence_after();
-                uint32_t r[kTile];
-#pragma unroll
-                for (int c4 = 0; c4 < kTile / 32; ++c4) tmem_ld32(tS + c4 * 32, r + c4 * 32);
+                uint32_t r[kFwdKeys];
+                tmem_ld32(tS, r);
+                tmem_ld32(tS + 32, r + 32);
                 tmem_wait_ld();
-                const int valid = w.nk - j * kTile;
-                if (valid < kTile) {
+                const int valid = w.nk - j * kFwdKeys;
+                if (valid < kFwdKeys) {
 #pragma unroll
-                    for (int i = 0; i < kTile; ++i)
+                    for (int i = 0; i < kFwdKeys; ++i)
                         if (i >= valid) r[i] = __float_as_uint(-INFINITY);
                 }
                 float m4[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) m4[i] = __uint_as_float(r[i]);
 #pragma unroll
-                for (int i = 4; i < kTile; i += 2)
+                for (int i = 4; i < kFwdKeys; i += 2)
                     m4[(i >> 1) & 3] = fmax3(m4[(i >> 1) & 3], __uint_as_float(r[i]), __uint_as_float(r[i + 1]));
                 const float mt = fmax3(fmax3(m4[0], m4[1], m4[2]), m4[3], m4[3]) * a.scale_log2;
-                bool rescale = false;
-                float alpha = 1.f;
                 if (j == w.t0) {
                     m_run = mt;
                 } else if (__any_sync(0xffffffffu, mt > m_run + 8.f)) {
                     const float mn = fmaxf(m_run, mt);
                     // every logit so far -inf: l = 0 and O = 0, nothing to scale
-                    alpha = m_run == -INFINITY ? 0.f : ex2(m_run - mn);
+                    const float alpha = m_run == -INFINITY ? 0.f : ex2(m_run - mn);
                     m_run = mn;
-                    l *= alpha;
-                    rescale = true;
+                    const uint64_t al = f2pack(alpha, alpha);
+                    lA = fmul2(lA, al);
+                    lB = fmul2(lB, al);
+                    // O holds the sum up to the step before once its PV is done (this step's waits for this warp)
+                    if (!(ok = wait.warp(&o_full[t][(ns - 1) & 1], ((ns - 1) >> 1) & 1, 0x4e))) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint32_t o[16];
+                        tmem_ld16(tO + c * 16, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                        tmem_st16(tO + c * 16, o);
+                    }
                 }
                 const float m_ref = m_run == -INFINITY ? 0.f : m_run;
-                const uint64_t scp = f2pack(a.scale_log2, a.scale_log2), nmp = f2pack(-m_ref, -m_ref);
-                uint64_t sA = 0ull, sB = 0ull;
+                const uint64_t nmp = f2pack(-m_ref, -m_ref);
 #pragma unroll
-                for (int c4 = 0; c4 < kTile / 32; ++c4) {
+                for (int c = 0; c < kFwdKeys / 32; ++c) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const uint64_t x2 = ffma2(
-                            f2pack(__uint_as_float(r[c4 * 32 + 2 * i]), __uint_as_float(r[c4 * 32 + 2 * i + 1])), scp, nmp);
+                        const int e = c * 32 + 2 * i;
                         float x0, x1;
-                        f2unpack(x2, x0, x1);
-                        const float p0 = ex2(x0), p1 = ex2(x1);
-                        if (i & 1) sB = fadd2(sB, f2pack(p0, p1));
-                        else sA = fadd2(sA, f2pack(p0, p1));
-                        pk[i] = pack2(T(), p0, p1);
+                        f2unpack(ffma2(f2pack(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), scp, nmp), x0, x1);
+                        x0 = ex2(x0);
+                        x1 = ex2(x1);
+                        if (i & 1) lB = fadd2(lB, f2pack(x0, x1));
+                        else lA = fadd2(lA, f2pack(x0, x1));
+                        pk[i] = pack2(T(), x0, x1);
                     }
-                    tmem_st16(tS + c4 * 16, pk);
-                }
-                float la, lb, lc, ld;
-                f2unpack(sA, la, lb);
-                f2unpack(sB, lc, ld);
-                l += (la + lc) + (lb + ld);
-                if (rescale) {
-#pragma unroll
-                    for (int c4 = 0; c4 < D / 32; ++c4) {
-                        uint32_t o[32];
-                        tmem_ld32(tO + c4 * 32, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-                        tmem_st32(tO + c4 * 32, o);
-                    }
+                    tmem_st16(tS + c * 16, pk);
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[t]);
+                if (lane == 0) mbar_arrive(&p_full[t][ns & 1]);
             }
             if (!ok) break;
+            float la, lb, lc, ld;
+            f2unpack(lA, la, lb);
+            f2unpack(lB, lc, ld);
+            const float l = (la + lc) + (lb + ld);
+            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a NaN sum stays one
+            const int row = t * kTile + wq * 32 + lane;
+            const bool store = row < w.r.nq;
+            int b, h, n;  // of this thread's row; behind the last one, of the tile's first
+            tile_row(a, w.r, w.hk, store ? row : 0, b, h, n);
+            const int64_t flat = ((int64_t)b * a.H + h) * a.N + n, part = w.split * (int64_t)a.B * a.H * a.N + flat;
+            T *o = static_cast<T *>(a.o) + b * a.oB + h * a.oH + n * a.oN;
+            float *po = a.part_o + part * D;
+            if (store) {
+                const float lse2 = l == 0.f ? -INFINITY : m_run + log2f(l);
+                if (a.splits > 1) a.part_lse[part] = lse2;
+                else if (a.lse) a.lse[flat] = lse2 * 0.6931471805599453f;
+            }
+            w = fwd_item(a, item + gridDim.x);  // while the last products run
             if (some) {
-                if (!(ok = wait.warp(&o_full[t], no & 1, 0x4a + t))) break;
-                ++no;
+                if (!(ok = wait.warp(&o_full[t][(ns - 1) & 1], ((ns - 1) >> 1) & 1, 0x4a + t))) break;
                 tc_fence_after();
             }
-            // all products of the item are done: the O rows leave through this tile's part of the Q buffer
-            const uint32_t stage = smem_u32(sQ + (buf * 2 + t) * TB) + wq * (TB / 4);
-            const int first = t * kTile + wq * 32, n_rows = w.r.nq - first;
-            const bool store = lane < n_rows;
-            int b, h, n;
-            tile_row(a, w.r, w.hk, store ? first + lane : 0, b, h, n);
-            const int64_t total = (int64_t)a.B * a.H * a.N, flat = ((int64_t)b * a.H + h) * a.N + n;
-            const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a NaN sum stays one
-            const float lse2 = l == 0.f ? -INFINITY : m_run + log2f(l);
-            T *o = static_cast<T *>(a.o);
-            auto o_row = [&](int i) {
-                int rb, rh, rn;
-                tile_row(a, w.r, w.hk, first + i, rb, rh, rn);
-                return o + rb * a.oB + rh * a.oH + rn * a.oN;
-            };
-            auto part_row = [&](int i) {
-                int rb, rh, rn;
-                tile_row(a, w.r, w.hk, first + i, rb, rh, rn);
-                return a.part_o + (w.split * total + ((int64_t)rb * a.H + rh) * a.N + rn) * D;
-            };
-            if (some) {
 #pragma unroll 1
-                for (int c = 0; c < D / 64; ++c) {
-                    uint32_t r[64];
-                    tmem_ld32(tO + c * 64, r);
-                    tmem_ld32(tO + c * 64 + 32, r + 32);
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t r[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) r[i] = 0u;
+                if (some) {
+                    tmem_ld32(tO + c * 32, r);
                     tmem_wait_ld();
-                    if (c == D / 64 - 1) {
+                    if (c == D / 32 - 1) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&o_empty[t]);
                     }
-                    float f[64];
-#pragma unroll
-                    for (int i = 0; i < 64; ++i) f[i] = __uint_as_float(r[i]) * inv;
-                    uint4 u[8];
-                    if (a.splits > 1) {
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) u[i] = bits4(f + x * 32 + 4 * i);
-                            store_staged<8>(stage, u, n_rows, [&](int i) { return part_row(i) + c * 64 + x * 32; });
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) u[i] = pack8<T>(f + 8 * i);
-                        store_staged<8>(stage, u, n_rows, [&](int i) { return o_row(i) + c * 64; });
-                    }
                 }
-                fence_async_smem();  // before a TMA load writes the buffer again
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&q_empty[buf]);
-            } else if (store) {
-                const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                for (int i = 0; i < D; i += 8) {
-                    if (a.splits > 1) store8(part_row(lane) + i, zero);
-                    else store8(o_row(lane) + i, zero);
-                }
-            }
-            if (store) {
-                if (a.splits > 1) a.part_lse[w.split * total + flat] = lse2;
-                else if (a.lse) a.lse[flat] = lse2 * 0.6931471805599453f;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * inv);
+                if (!store) continue;
+                if (a.splits > 1) store_row<32>(po + c * 32, r);
+                else store_row<T, 32>(o + c * 32, reinterpret_cast<const float *>(r), a.wide);
             }
         }
     }
@@ -480,18 +474,18 @@ cudaError_t cross_fwd_error(int32_t *err, bool clear)
 }
 
 // Key ranges per row tile: the count with the least modelled time, in steps of
-// one 128-key tile (some 1.2 us a CTA).  An item costs its tiles and about two
-// more for its Q rows and epilogue; a split adds a launch (about 3 steps) and
+// one 64-key tile (some 0.7 us a CTA).  An item costs its tiles and about four
+// more for its Q rows and epilogue; a split adds a launch (about 5 steps) and
 // the partial outputs' traffic.
 int cross_fwd_splits(int64_t sets, int64_t pairs, int64_t M, int64_t rows_total, int D, int sms)
 {
-    const int64_t tiles = (M + kTile - 1) / kTile, items = sets * pairs;
+    const int64_t tiles = (M + kFwdKeys - 1) / kFwdKeys, items = sets * pairs;
     int best = 1;
     double least = 0.0;
     for (int64_t s = 1; s <= tiles && s <= 128 && (s == 1 || items * (s - 1) < sms); ++s) {
         const double waves = (double)((items * s + sms - 1) / sms);
-        double t = waves * (double)((tiles + s - 1) / s + 2);
-        if (s > 1) t += 3.0 + (double)(s * rows_total) * D * 8.0 / 6e6;
+        double t = waves * (double)((tiles + s - 1) / s + 4);
+        if (s > 1) t += 5.0 + (double)(s * rows_total) * D * 8.0 / 4e6;
         if (s == 1 || t < least) {
             least = t;
             best = (int)s;

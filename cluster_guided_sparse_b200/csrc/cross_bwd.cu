@@ -54,13 +54,6 @@ constexpr int kTiles = 7;    // tiles in shared memory, both kernels
 constexpr int kFloats = 5 * kT;
 constexpr size_t bwd_smem(int D) { return (size_t)kTiles * kT * D * 2 + kFloats * 4 + 256; }
 
-__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 // Column of 16-element step k of p (ds: 32 further on) as an A operand: the 64
 // values of each half of the warps sit, packed, in the half's own columns of S.
 __device__ __forceinline__ uint32_t half_col(int k) { return (uint32_t)((k >> 2) * 64 + (k & 3) * 8); }
@@ -130,8 +123,9 @@ template <typename T, int D>
 __global__ void __launch_bounds__(256) cross_rows_kernel(const __grid_constant__ CrossArgs a)
 {
     constexpr int LPR = D / 8, RPP = 256 / LPR;  // lanes a row, rows a pass
-    const int set = blockIdx.x / a.tiles, rt = blockIdx.x % a.tiles, hk = set % a.Hk;
-    const RowTile w = row_tile<kT>(a, set / a.Hk, hk, rt);
+    int rt, hk;
+    const int set = a.by_tiles((int)blockIdx.x, rt), bk = a.by_Hk(set, hk);
+    const RowTile w = row_tile<kT>(a, bk, hk, rt);
     const int c8 = threadIdx.x % LPR, row0 = threadIdx.x / LPR;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -173,45 +167,42 @@ struct DqItem {
     RowTile r;
 };
 
-__device__ __forceinline__ DqItem dq_item(const CrossArgs &a, int item)
+__device__ __noinline__ DqItem dq_item(const CrossArgs &a, int item)
 {
     DqItem w;
-    const int rt = item % a.tiles, rest = item / a.tiles;
-    w.split = rest % a.dq_splits;
-    const int set = rest / a.dq_splits;
-    w.bk = set / a.Hk;
-    w.hk = set % a.Hk;
+    int rt;
+    const int set = a.by_splits(a.by_tiles(item, rt), w.split);
+    w.bk = a.by_Hk(set, w.hk);
     w.r = row_tile<kT>(a, w.bk, w.hk, rt);
     w.at = ((int64_t)set * a.tiles + rt) * kT;
     w.nk = keys_of(a, w.bk);
-    const int kt = (w.nk + kT - 1) / kT;
-    w.t0 = (int)((int64_t)kt * w.split / a.dq_splits);
-    w.t1 = (int)((int64_t)kt * (w.split + 1) / a.dq_splits);
+    split_range((w.nk + kT - 1) / kT, w.split, a.by_splits, w.t0, w.t1);
     return w;
 }
 
-// A CTA's key tiles in order, over its items.
+// A CTA's key tiles in order, over its items; by a whole warp.
 struct DqStep {
-    int item, j;
-    DqItem w;
+    int item, j, t0, t1;
     __device__ __forceinline__ bool seek(const CrossArgs &a, int from, int items)
     {
+#pragma unroll 1
         for (item = from; item < items; item += gridDim.x) {
-            w = dq_item(a, item);
-            j = w.t0;
-            if (w.t0 < w.t1) return true;
+            const DqItem w = dq_item(a, item);
+            j = t0 = uniform(w.t0);
+            t1 = uniform(w.t1);
+            if (t0 < t1) return true;
         }
         return false;
     }
     __device__ __forceinline__ bool next(const CrossArgs &a, int items)
     {
-        return ++j < w.t1 || seek(a, item + gridDim.x, items);
+        return ++j < t1 || seek(a, item + gridDim.x, items);
     }
 };
 
 // One persistent CTA per SM; item = 128 rows of a key set and a key range.  TMEM:
 // X0 [0,128), X1 [128,256), sum t k [256,256+D), sum p k [384,384+D).  Shared
-// memory: 2 Q tiles (the next item's comes early; dq leaves through it), 1 dO
+// memory: 2 Q tiles (the next item's comes early), 1 dO
 // tile, rings of 3 K and 1 V tiles.  Warps 0-3 take the keys 0-63 of a tile,
 // warps 4-7 the keys 64-127, one thread per row and half; warps 8, 9, 10 load
 // Q and dO, K, V; warp 11 issues.
@@ -231,7 +222,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     };
     static_assert(sizeof(Barriers) <= 256, "room kept in bwd_smem");
     Barriers &bar = *reinterpret_cast<Barriers *>(smem_raw + kTiles * TB + kFloats * 4);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (sQ & 1023u) {  // uniform
         if (threadIdx.x == 0) set_error(g_cross_bwd_err, kErrRange, 0x70);
         return;
@@ -239,7 +230,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.q_full[i], 1);
-            mbar_init(&bar.q_empty[i], 8);
+            mbar_init(&bar.q_empty[i], 1);
         }
         for (int i = 0; i < 3; ++i) {
             mbar_init(&bar.k_full[i], 1);
@@ -259,13 +250,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     bwd_prologue(warp, &bar.tmem_base);
-    const uint32_t tmem = bar.tmem_base;
+    const uint32_t tmem = uniform(bar.tmem_base);
     const Waiter wait{&bar.abort, g_cross_bwd_err};
 
     if (warp == 8) {
         // ------------------------------------------------------------ Q, dO rows
         int qi = 0;
         bool ok = true;
+#pragma unroll 1
         for (int item = blockIdx.x; item < items; item += gridDim.x) {
             const DqItem w = dq_item(a, item);
             if (w.t0 == w.t1) continue;
@@ -282,82 +274,74 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
     } else if (warp == 9 || warp == 10) {
         // ------------------------------------------------------------ K rows, V rows
-        auto fill = [&](auto &ring, const CUtensorMap *map, const void *src, int64_t sB, int64_t sH, int64_t sN,
-                        uint32_t smem) {
-            bool ok = true;
-            for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
-                const DqItem w = dq_item(a, item);
-                const T *base = static_cast<const T *>(src) + w.bk * sB + w.hk * sH;
-                const int32_t *list = a.idx ? a.idx + (int64_t)w.bk * a.M : nullptr;
-                for (int j = w.t0; j < w.t1; ++j) {
-                    if (!(ok = ring.acquire(wait, 0x51))) break;
-                    const uint32_t dst = smem + ring.slot * TB;
-                    if (tma_keys(a, w.nk, j)) {
-                        ring.template tma<D>(true, dst, map, j * kT, w.hk, w.bk);
-                    } else {
-                        copy_keys<T, D, 32>(list, w.nk, j, base, sN, dst, lane);
-                        ring.issued();
-                    }
-                }
-            }
-            ring.finish(!ok);
-        };
-        if (warp == 9) {
-            RingFill<3> ring(bar.k_full, bar.k_empty);
-            fill(ring, &m.k, a.k, a.kB, a.kH, a.kN, sK);
-        } else {
-            RingFill<1> ring(&bar.v_full, &bar.v_empty);
-            fill(ring, &m.v, a.v, a.vB, a.vH, a.vN, sV);
-        }
+        auto decode = [&](int item) { return dq_item(a, item); };
+        if (warp == 9)
+            fill_keys<T, D, kT>(a, RingFill<3>(bar.k_full, bar.k_empty), &m.k, a.k, a.kB, a.kH, a.kN, sK, items, wait, 0x51,
+                                decode);
+        else
+            fill_keys<T, D, kT>(a, RingFill<1>(&bar.v_full, &bar.v_empty), &m.v, a.v, a.vB, a.vH, a.vN, sV, items, wait,
+                                0x5c, decode);
     } else if (warp == 11) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            RingRead<3> kr;
-            DqStep cur, nxt;
-            int ns = 0, qi = 0;  // steps, items begun
-            auto issue_s = [&](const DqStep &st, int step, int &slot) {
-                const int item = st.j == st.w.t0 ? qi++ : qi - 1;
-                if (!wait(&bar.q_full[item & 1], (item >> 1) & 1, 0x52)) return false;
-                slot = kr.slot;
-                if (!wait(&bar.k_full[slot], kr.use & 1, 0x53)) return false;
-                kr.next();
-                tc_fence_after();
+        // (by the whole warp, one lane issuing, as in cross_attn.cu)
+        RingRead<3> kr;
+        DqStep cur, nxt;
+        int ns = 0, qi = 0;  // steps, items begun
+        auto issue_s = [&](const DqStep &st, int step, int &slot) {
+            if (st.j == st.t0) ++qi;
+            const int item = qi - 1;
+            if (!wait.warp(&bar.q_full[item & 1], (item >> 1) & 1, 0x52)) return false;
+            slot = kr.slot;
+            if (!wait.warp(&bar.k_full[slot], kr.use & 1, 0x53)) return false;
+            kr.next();
+            tc_fence_after();
+            const bool last = st.j + 1 == st.t1;
+            if (elect_one()) {
                 tile_product<T, D>(tmem + (step & 1) * 128, sQ + (item & 1) * TB, sK + slot * TB);
                 mma_commit(&bar.s_full);
-                return true;
-            };
-            auto issue_dp = [&](const DqStep &st, int step) {
-                if (!wait(&bar.o_full, (qi - 1) & 1, 0x54) || !wait(&bar.v_full, step & 1, 0x55)) return false;
-                tc_fence_after();
+                if (last) mma_commit(&bar.q_empty[item & 1]);
+            }
+            __syncwarp();
+            return true;
+        };
+        auto issue_dp = [&](const DqStep &st, int step) {
+            if (!wait.warp(&bar.o_full, (qi - 1) & 1, 0x54) || !wait.warp(&bar.v_full, step & 1, 0x55)) return false;
+            tc_fence_after();
+            const bool last = st.j + 1 == st.t1;
+            if (elect_one()) {
                 tile_product<T, D>(tmem + ((step & 1) ^ 1) * 128, sO, sV);
                 mma_commit(&bar.dp_full);
                 mma_commit(&bar.v_empty);
-                if (st.j + 1 == st.w.t1) mma_commit(&bar.o_empty);
-                return true;
-            };
-            int ks = 0, kn = 0;
-            bool more = cur.seek(a, blockIdx.x, items);
-            bool ok = more && issue_s(cur, 0, ks) && issue_dp(cur, 0);
-            while (ok && more) {
-                nxt = cur;
-                more = nxt.next(a, items);
-                // dP of this step has been read: the buffer is free for the next S
-                if (more && !(ok = wait(&bar.dp_read, ns & 1, 0x56) && issue_s(nxt, ns + 1, kn))) break;
-                if (!(ok = wait(&bar.ds_full, ns & 1, 0x57))) break;
-                tc_fence_after();
-                const uint32_t p = tmem + (ns & 1) * 128;
-                const bool first = cur.j == cur.w.t0;
+                if (last) mma_commit(&bar.o_empty);
+            }
+            __syncwarp();
+            return true;
+        };
+        int ks = 0, kn = 0;
+        bool more = cur.seek(a, blockIdx.x, items);
+        bool ok = more && issue_s(cur, 0, ks) && issue_dp(cur, 0);
+#pragma unroll 1
+        while (ok && more) {
+            nxt = cur;
+            more = nxt.next(a, items);
+            // dP of this step has been read: the buffer is free for the next S
+            if (more && !(ok = wait.warp(&bar.dp_read, ns & 1, 0x56) && issue_s(nxt, ns + 1, kn))) break;
+            if (!(ok = wait.warp(&bar.ds_full, ns & 1, 0x57))) break;
+            tc_fence_after();
+            const uint32_t p = tmem + (ns & 1) * 128;
+            const bool first = cur.j == cur.t0, last = cur.j + 1 == cur.t1;
+            if (elect_one()) {
                 tile_accumulate<T, D>(tmem + 256, p + 32, sK + ks * TB, first);
                 tile_accumulate<T, D>(tmem + 384, p, sK + ks * TB, first);
                 mma_commit(&bar.k_empty[ks]);
-                if (cur.j + 1 == cur.w.t1) mma_commit(&bar.dq_full);
-                if (more && !(ok = issue_dp(nxt, ns + 1))) break;
-                cur = nxt;
-                ks = kn;
-                ++ns;
+                if (last) mma_commit(&bar.dq_full);
             }
+            __syncwarp();
+            if (more && !(ok = issue_dp(nxt, ns + 1))) break;
+            cur = nxt;
+            ks = kn;
+            ++ns;
         }
-        __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax and epilogue
         const int half = warp >> 2, wq = warp & 3, row = wq * 32 + lane;
@@ -365,11 +349,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         int ns = 0, qi = 0;
         bool ok = true;
         const uint64_t scp = f2pack(a.scale_log2, a.scale_log2);
+#pragma unroll 1
         for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
             const DqItem w = dq_item(a, item);
             const float nl = a.nlse[w.at + row], nd = a.ndelta[w.at + row];
             const uint64_t nlp = f2pack(nl, nl), ndp = f2pack(nd, nd);
             uint64_t dA = 0ull, dB = 0ull;
+#pragma unroll 1
             for (int j = w.t0; j < w.t1; ++j, ++ns) {
                 const uint32_t tS = tmem + lane_off + (ns & 1) * 128 + half * 64;
                 const uint32_t tP = tmem + lane_off + ((ns & 1) ^ 1) * 128 + half * 64;
@@ -420,34 +406,25 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 if (lane == 0) mbar_arrive(&bar.ds_full);
             }
             if (!ok) break;
-            const int n_rows = w.r.nq - wq * 32;
-            const bool store = lane < n_rows;
+            const bool store = row < w.r.nq;
             int b, h, n;
             tile_row(a, w.r, w.hk, store ? row : 0, b, h, n);
-            const int64_t total = (int64_t)a.B * a.H * a.N, flat = ((int64_t)b * a.H + h) * a.N + n;
-            T *dq = static_cast<T *>(a.dq);
-            auto dq_row = [&](int i) {
-                int rb, rh, rn;
-                tile_row(a, w.r, w.hk, wq * 32 + i, rb, rh, rn);
-                return dq + rb * a.dqB + rh * a.dqH + rn * a.dqN + half * (D / 2);
-            };
-            auto part_row = [&](float *part, int i) {
-                int rb, rh, rn;
-                tile_row(a, w.r, w.hk, wq * 32 + i, rb, rh, rn);
-                return part + (w.split * total + ((int64_t)rb * a.H + rh) * a.N + rn) * D + half * (D / 2);
-            };
+            const int64_t part = w.split * (int64_t)a.B * a.H * a.N + ((int64_t)b * a.H + h) * a.N + n;
+            T *dq = static_cast<T *>(a.dq) + b * a.dqB + h * a.dqH + n * a.dqN + half * (D / 2);
+            float *pt = a.part_t + part * D + half * (D / 2), *pe = a.part_e + part * D + half * (D / 2);
             if (w.t0 == w.t1) {  // no keys
                 if (store) {
                     const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
                     for (int i = 0; i < D / 2; i += 8) {
                         if (a.dq_splits > 1) {
-                            store8(part_row(a.part_t, lane) + i, zero);
-                            store8(part_row(a.part_e, lane) + i, zero);
+                            store8(pt + i, zero);
+                            store8(pe + i, zero);
                         } else {
-                            store8(dq_row(lane) + i, zero);
+                            store8(dq + i, zero);
                         }
                     }
-                    if (a.dq_splits > 1 && half == 0) a.part_delta[w.split * total + flat] = 0.f;
+                    if (a.dq_splits > 1 && half == 0) a.part_delta[part] = 0.f;
                 }
                 continue;
             }
@@ -466,14 +443,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             delta = pair[0] + pair[kT];
             if (half == 0) {
                 if (a.dq_splits > 1) {
-                    if (store) a.part_delta[w.split * total + flat] = delta;
+                    if (store) a.part_delta[part] = delta;
                 } else {
                     a.ndelta[w.at + row] = nd - delta;
                 }
             }
             if (!(ok = wait.warp(&bar.dq_full, qi & 1, 0x5b))) break;
             tc_fence_after();
-            const uint32_t stage = sQ + (qi & 1) * TB + warp * (TB / 8);
             if (a.dq_splits > 1) {
 #pragma unroll 1
                 for (int x = 0; x < 2 * (D / 64); ++x) {
@@ -481,22 +457,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     uint32_t r[32];
                     tmem_ld32(tmem + lane_off + 256 + e * 128 + half * (D / 2) + c * 32, r);
                     tmem_wait_ld();
-                    // fp32: 16 columns a pass at D = 64, where a warp has 2 KB to stage in
-#pragma unroll
-                    for (int y = 0; y < 128 / D; ++y) {
-                        constexpr int CH = D / 16;
-                        uint4 u[CH];
-#pragma unroll
-                        for (int i = 0; i < CH; ++i)
-                            u[i] = make_uint4(r[(y * CH + i) * 4], r[(y * CH + i) * 4 + 1], r[(y * CH + i) * 4 + 2],
-                                              r[(y * CH + i) * 4 + 3]);
-                        store_staged<CH>(stage, u, n_rows, [&](int i) {
-                            return part_row(e ? a.part_e : a.part_t, i) + c * 32 + y * CH * 4;
-                        });
-                    }
+                    if (store) store_row<32>((e ? pe : pt) + c * 32, r);
                 }
             } else {
-                uint4 u[D / 16];
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
                     uint32_t r[32], e[32];
@@ -507,15 +470,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         f[i] = fmaf(-delta, __uint_as_float(e[i]), __uint_as_float(r[i])) * a.scale;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) u[c * 4 + i] = pack8<T>(f + 8 * i);
+                    if (store) store_row<T, 32>(dq + c * 32, f, a.wide);
                 }
-                store_staged<D / 16>(stage, u, n_rows, dq_row);
             }
             tc_fence_before();
-            fence_async_smem();  // before a TMA load writes the Q buffer again
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.q_empty[qi & 1]);
             ++qi;
         }
     }
@@ -573,14 +531,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     };
     static_assert(sizeof(Barriers) <= 256, "room kept in bwd_smem");
     Barriers &bar = *reinterpret_cast<Barriers *>(smem_raw + kTiles * TB + kFloats * 4);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
     const int kt = blockIdx.x % key_tiles, rest = blockIdx.x / key_tiles;
     const int split = rest % a.dkv_splits, set = rest / a.dkv_splits;
     const int bk = set / a.Hk, hk = set % a.Hk;
     const int nk = keys_of(a, bk);
-    const int i0 = (int)((int64_t)a.tiles * split / a.dkv_splits);
-    const int i1 = (int)((int64_t)a.tiles * (split + 1) / a.dkv_splits);
+    int i0, i1;
+    split_range(a.tiles, split, a.by_dkv_splits, i0, i1);
     // uniform for the CTA: no keys here, or a base that is not aligned
     if (kt * kT >= nk) return;
     if (sK & 1023u) {
@@ -606,12 +564,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     bwd_prologue(warp, &bar.tmem_base);
-    const uint32_t tmem = bar.tmem_base;
+    const uint32_t tmem = uniform(bar.tmem_base);
     const Waiter wait{&bar.abort, g_cross_bwd_err};
 
     if (warp == 8) {
         // ------------------------------------------------------------ K, V
-        if (tma_keys(a, nk, kt)) {
+        if (tma_keys<kT>(a, nk, kt)) {
             if (lane == 0) {
                 mbar_expect_tx(&bar.kv_full, 2 * TB);
                 tma_tile<D>(sK, &m.k, kt * kT, hk, bk, &bar.kv_full);
@@ -619,8 +577,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
         } else {
             const int32_t *list = a.idx ? a.idx + (int64_t)bk * a.M : nullptr;
-            copy_keys<T, D, 32>(list, nk, kt, static_cast<const T *>(a.k) + bk * a.kB + hk * a.kH, a.kN, sK, lane);
-            copy_keys<T, D, 32>(list, nk, kt, static_cast<const T *>(a.v) + bk * a.vB + hk * a.vH, a.vN, sV, lane);
+            copy_keys<T, D, kT>(list, nk, kt, static_cast<const T *>(a.k) + bk * a.kB + hk * a.kH, a.kN, sK);
+            copy_keys<T, D, kT>(list, nk, kt, static_cast<const T *>(a.v) + bk * a.vB + hk * a.vH, a.vN, sV);
             cp_async_commit();
             cp_async_wait_all();
             fence_async_smem();
@@ -640,6 +598,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const uint32_t smem = q ? sQ : sO;
         bool ok = true;
         int u = 0;
+#pragma unroll 1
         for (int i = i0; i < i1; ++i, ++u) {
             const int slot = u % ns, use = u / ns;
             if (use > 0 && !(ok = wait.warp(&empty[slot], (use - 1) & 1, 0x60))) break;
@@ -652,45 +611,53 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             for (int i = max(0, u - ns); i < u; ++i) drain(&full[i % ns], (i / ns) & 1);
     } else if (warp == 11) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            RingRead<3> qr;
-            RingRead<2> dr;
-            auto issue_s = [&](int u, int &slot) {
-                slot = qr.slot;
-                if (!wait(&bar.q_full[slot], qr.use & 1, 0x61)) return false;
-                qr.next();
-                tc_fence_after();
+        RingRead<3> qr;
+        RingRead<2> dr;
+        const int n = uniform(i1 - i0);
+        auto issue_s = [&](int u, int &slot) {
+            slot = qr.slot;
+            if (!wait.warp(&bar.q_full[slot], qr.use & 1, 0x61)) return false;
+            qr.next();
+            tc_fence_after();
+            if (elect_one()) {
                 tile_product<T, D>(tmem + (u & 1) * 128, sK, sQ + slot * TB);
                 mma_commit(&bar.s_full);
-                return true;
-            };
-            auto issue_dp = [&](int u, int &slot) {
-                slot = dr.slot;
-                if (!wait(&bar.o_full[slot], dr.use & 1, 0x62)) return false;
-                dr.next();
-                tc_fence_after();
+            }
+            __syncwarp();
+            return true;
+        };
+        auto issue_dp = [&](int u, int &slot) {
+            slot = dr.slot;
+            if (!wait.warp(&bar.o_full[slot], dr.use & 1, 0x62)) return false;
+            dr.next();
+            tc_fence_after();
+            if (elect_one()) {
                 tile_product<T, D>(tmem + ((u & 1) ^ 1) * 128, sV, sO + slot * TB);
                 mma_commit(&bar.dp_full);
-                return true;
-            };
-            int qs = 0, qn = 0, os = 0;
-            bool ok = wait(&bar.kv_full, 0, 0x63) && issue_s(0, qs) && issue_dp(0, os);
-            for (int u = 0; ok && u < i1 - i0; ++u) {
-                const bool more = u + 1 < i1 - i0;
-                if (more && !(ok = wait(&bar.dp_read, u & 1, 0x64) && issue_s(u + 1, qn))) break;
-                if (!(ok = wait(&bar.ds_full, u & 1, 0x65))) break;
-                tc_fence_after();
-                const uint32_t p = tmem + (u & 1) * 128;
+            }
+            __syncwarp();
+            return true;
+        };
+        int qs = 0, qn = 0, os = 0;
+        bool ok = wait.warp(&bar.kv_full, 0, 0x63) && issue_s(0, qs) && issue_dp(0, os);
+#pragma unroll 1
+        for (int u = 0; ok && u < n; ++u) {
+            const bool more = u + 1 < n;
+            if (more && !(ok = wait.warp(&bar.dp_read, u & 1, 0x64) && issue_s(u + 1, qn))) break;
+            if (!(ok = wait.warp(&bar.ds_full, u & 1, 0x65))) break;
+            tc_fence_after();
+            const uint32_t p = tmem + (u & 1) * 128;
+            if (elect_one()) {
                 tile_accumulate<T, D>(tmem + 256, p, sO + os * TB, u == 0);
                 mma_commit(&bar.o_empty[os]);
                 tile_accumulate<T, D>(tmem + 384, p + 32, sQ + qs * TB, u == 0);
                 mma_commit(&bar.q_empty[qs]);
                 if (!more) mma_commit(&bar.acc_full);
-                else if (!(ok = issue_dp(u + 1, os))) break;
-                qs = qn;
             }
+            __syncwarp();
+            if (more && !(ok = issue_dp(u + 1, os))) break;
+            qs = qn;
         }
-        __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax and epilogue
         const int half = warp >> 2, wq = warp & 3, key = wq * 32 + lane;
@@ -699,6 +666,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         bool ok = true;
         RingRead<3> qr;  // nlse, ndelta come with the Q, dO tiles
         RingRead<2> dr;
+#pragma unroll 1
         for (int u = 0; u < i1 - i0; ++u) {
             const ulonglong2 *nl = reinterpret_cast<const ulonglong2 *>(s_nl + qr.slot * kT + half * 64);
             const ulonglong2 *nd = reinterpret_cast<const ulonglong2 *>(s_nd + dr.slot * kT + half * 64);

@@ -21,7 +21,32 @@ namespace scope {
 namespace op {
 
 struct CrossMaps {
-    CUtensorMap q, k, v, d;  // [B][H][N][D] boxes of 128 rows x 64 columns, 128B swizzle
+    CUtensorMap q, k, v, d;  // [B][H][N][D] boxes of 128 (forward k, v: kFwdKeys) rows x 64 columns, 128B swizzle
+};
+
+constexpr int kFwdKeys = 64;  // keys of a tile of the forward kernel
+
+// n / d for 0 <= n < 2^31 without a division: a decoded work item costs some
+// hundred clocks with these and 1500 with the divide instructions' sequences.
+struct Div {
+    uint32_t mul;
+    int shift, d;
+    Div() = default;
+    explicit Div(int by) : mul(0), shift(0), d(by < 1 ? 1 : by)
+    {
+        while (((int64_t)1 << shift) < d) ++shift;
+        mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << shift) - d)) / d + 1);
+    }
+    __device__ __forceinline__ int operator()(int n) const
+    {
+        return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift);
+    }
+    __device__ __forceinline__ int operator()(int n, int &rest) const
+    {
+        const int q = (*this)(n);
+        rest = n - q * d;
+        return q;
+    }
 };
 
 struct CrossArgs {
@@ -34,9 +59,12 @@ struct CrossArgs {
     int B, Bk, H, Hk, G, N, M;
     int heads;                 // heads whose rows read one key set: G, or B * G
     int fold;                  // how rows are cut into tiles
+    int wide;                  // rows of o (backward: dq) start on 32 bytes
     int tma_kv, tma_rows;      // whether the k, v maps are valid, and the q, d ones (by head only)
     int sets;                  // Bk * Hk
     int pairs, splits;         // 256-row tiles per set, key ranges (forward)
+    // per: row tiles of a head; tiles, splits: of the forward's, of the dq kernel's items
+    Div by_N, by_G, by_Hk, by_per, by_tiles, by_splits, by_dkv_splits;
     int items;                 // sets * splits * pairs
     float scale, scale_log2;   // scale, scale * log2(e)
     float *part_o;             // [splits][B*H*N][D], normalised per split (splits > 1)
@@ -71,20 +99,15 @@ __device__ __forceinline__ RowTile row_tile(const CrossArgs &a, int bk, int hk, 
     int hh;
     if (a.fold) {
         const int r0 = rt * T;
-        hh = r0 / a.N;
-        w.n = r0 - hh * a.N;
+        hh = a.by_N(r0, w.n);
         w.nq = min(T, a.heads * a.N - r0);
     } else {
-        const int per = (a.N + T - 1) / T;
-        hh = rt / per;
-        w.n = (rt - hh * per) * T;
+        hh = a.by_per(rt, w.n);
+        w.n *= T;
         w.nq = min(T, a.N - w.n);
     }
     w.b = bk;
-    if (a.Bk != a.B) {
-        w.b = hh / a.G;
-        hh -= w.b * a.G;
-    }
+    if (a.Bk != a.B) w.b = a.by_G(hh, hh);
     w.h = hk * a.G + hh;
     return w;
 }
@@ -96,10 +119,8 @@ __device__ __forceinline__ void tile_row(const CrossArgs &a, const RowTile &w, i
     h = w.h;
     n = w.n + i;
     if (n >= a.N) {  // folded: a later head
-        const int step = n / a.N;
-        n -= step * a.N;
-        h += step;
-        const int over = (h - hk * a.G) / a.G;
+        h += a.by_N(n, n);
+        const int over = a.by_G(h - hk * a.G);
         b += over;
         h -= over * a.G;
     }
@@ -108,7 +129,7 @@ __device__ __forceinline__ void tile_row(const CrossArgs &a, const RowTile &w, i
 // Where (batch entry b, head h, query n) sits among its set's padded rows.
 __device__ __forceinline__ int64_t padded_row(const CrossArgs &a, int b, int h, int n)
 {
-    const int hk = h / a.G, shared = a.Bk != a.B;
+    const int hk = a.by_G(h), shared = a.Bk != a.B;
     const int hh = (shared ? b * a.G : 0) + h - hk * a.G, set = (shared ? 0 : b) * a.Hk + hk;
     const int64_t at = a.fold ? (int64_t)hh * a.N + n : (int64_t)hh * ((a.N + 127) / 128 * 128) + n;
     return (int64_t)set * a.tiles * 128 + at;
@@ -119,6 +140,18 @@ __device__ __forceinline__ int keys_of(const CrossArgs &a, int bk)
 {
     if (a.idx) return a.cnt[bk];
     return a.kv_len ? min(max(a.kv_len[bk], 0), a.M) : a.M;
+}
+
+// A value that is the same in all lanes, as one that the compiler knows to be.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// Tiles [t0, t1) of range `split` of `by.d` even ranges of n tiles.
+__device__ __forceinline__ void split_range(int n, int split, const Div &by, int &t0, int &t1)
+{
+    int rest;
+    const int base = by(n, rest);
+    t0 = base * split + min(split, rest);
+    t1 = t0 + base + (split < rest ? 1 : 0);
 }
 
 // Byte offset of 16-byte chunk `c` of row `r` in a [rows][D] tile of 16-bit
@@ -145,29 +178,44 @@ __device__ __forceinline__ uint32_t idesc16<__half>(int n, bool b_mn_major)
 
 // Bounded mbarrier wait of these kernels: by one lane, or by a whole warp, all
 // of whose lanes get the same answer (so a warp never splits around its
-// warp-wide instructions when a wait gives up).
+// warp-wide instructions when a wait gives up).  A look at a barrier takes some
+// 60 clocks, so a warp that needs several looks at all of them first (`all`).
+// The loop is a call: inlined at each wait it made the kernels' code several
+// times as long, and the roles, which run in turn, ran out of the instruction
+// caches (a ready wait of the issuer took 160 clocks instead of 45).
+static __device__ __noinline__ bool wait_longer(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int32_t *err, int where)
+{
+    return tc::mbar_wait(bar, parity, abort_flag, err, where);
+}
+
 struct Waiter {
     volatile int *abort_flag;
     int32_t *err;
     __device__ __forceinline__ bool operator()(uint64_t *bar, uint32_t parity, int where) const
     {
-        return tc::mbar_wait(bar, parity, abort_flag, err, where);
+        return tc::mbar_try_wait(bar, parity) || wait_longer(bar, parity, abort_flag, err, where);
     }
     __device__ __forceinline__ bool warp(uint64_t *bar, uint32_t parity, int where) const
     {
-        return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, abort_flag, err, where));
+        return __all_sync(0xffffffffu, (*this)(bar, parity, where));
+    }
+    __device__ __forceinline__ bool all(uint64_t *b0, uint32_t p0, int w0, uint64_t *b1, uint32_t p1, int w1) const
+    {
+        const bool r0 = tc::mbar_try_wait(b0, p0), r1 = tc::mbar_try_wait(b1, p1);
+        if (__all_sync(0xffffffffu, r0 && r1)) return true;
+        return warp(b0, p0, w0) && warp(b1, p1, w1);
     }
 };
 
-// TMA load of rows [n, n + 128) of head (b, h) into a swizzled tile.
-template <int D>
+// TMA load of rows [n, n + ROWS) of head (b, h) into a swizzled tile.
+template <int D, int ROWS = 128>
 __device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap *m, int n, int h, int b, uint64_t *bar)
 {
 #pragma unroll
     for (int x = 0; x < D / 64; ++x)
         asm volatile(
             "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-            " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst + x * (128 * 128)),
+            " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst + x * (ROWS * 128)),
             "l"(reinterpret_cast<uint64_t>(m)), "r"(x * 64), "r"(n), "r"(h), "r"(b), "r"(tc::smem_u32(bar))
             : "memory");
 }
@@ -181,9 +229,8 @@ __device__ __forceinline__ void drain(uint64_t *full, uint32_t parity)
     }
 }
 
-// Ring of shared-memory stages filled by one or more whole warps.  A stage
-// filled by cp.async is announced (one arrival per warp) once its copies landed,
-// which is checked after the next stage's copies were issued, so two are in
+// Ring of shared-memory stages filled by one warp.  A stage filled by cp.async is
+// announced once its copies landed, which is checked after the next stage's copies were issued, so two are in
 // flight; a stage filled by TMA announces itself.
 template <int NS>
 struct RingFill {
@@ -221,18 +268,14 @@ struct RingFill {
         pending = slot;
         advance();
     }
-    // Fills the stage by TMA; of several warps one is the lead.
-    template <int D>
-    __device__ __forceinline__ void tma(bool lead, uint32_t dst, const CUtensorMap *m, int n, int h, int b)
+    // Fills the stage by TMA.
+    template <int D, int ROWS>
+    __device__ __forceinline__ void tma(uint32_t dst, const CUtensorMap *m, int n, int h, int b)
     {
         if (pending >= 0) flush();
         if ((threadIdx.x & 31) == 0) {
-            if (lead) {
-                tc::mbar_expect_tx(&full[slot], 128 * D * 2);
-                tma_tile<D>(dst, m, n, h, b, &full[slot]);
-            } else {
-                tc::mbar_arrive(&full[slot]);
-            }
+            tc::mbar_expect_tx(&full[slot], ROWS * D * 2);
+            tma_tile<D, ROWS>(dst, m, n, h, b, &full[slot]);
         }
         __syncwarp();
         advance();
@@ -268,7 +311,7 @@ struct RingRead {
 // Copies the first `fill` rows of a row tile (element strides sB, sH, sN) into
 // swizzled tiles of 128 rows, rows from w.nq on as zeros, by one warp.
 template <typename T, int D>
-__device__ __forceinline__ void copy_rows(const CrossArgs &a, const RowTile &w, int hk, int fill, const T *src, int64_t sB,
+__device__ __noinline__ void copy_rows(const CrossArgs &a, const RowTile &w, int hk, int fill, const T *src, int64_t sB,
                                           int64_t sH, int64_t sN, uint32_t dst)
 {
     constexpr int CH = D / 8, RPI = 32 / CH;
@@ -304,67 +347,89 @@ __device__ __forceinline__ void load_rows(const CrossArgs &a, const RowTile &w, 
     __syncwarp();
 }
 
-// Whether the 128 keys of tile j can come by TMA.
+// Whether the keys of tile j (of ROWS keys) can come by TMA.
+template <int ROWS>
 __device__ __forceinline__ bool tma_keys(const CrossArgs &a, int nk, int j)
 {
-    return a.tma_kv && !a.idx && (nk == a.M || nk - j * 128 >= 128);
+    return a.tma_kv && !a.idx && (nk == a.M || nk - j * ROWS >= ROWS);
 }
 
-// One warp's rows through shared memory to global memory: each lane holds CH
-// 16-byte chunks of its own row; they leave as whole row segments.  `dst(i)`
-// is the address of row i's segment; rows from n_rows on are dropped.
-template <int CH, typename Dst>
-__device__ __forceinline__ void store_staged(uint32_t stage, const uint4 *v, int n_rows, Dst dst)
+// 16 values to 32 bytes of 16-bit elements, 8 to 32 bytes of fp32: whole sectors
+// of a row from one thread.  (Rows that go through shared memory leave in longer
+// segments, but the tensor cores keep it busy: 3100 clocks a 128-row tile.)
+__device__ __forceinline__ void store32(void *p, const uint32_t *u)
 {
-    const int lane = threadIdx.x & 31;
-    auto at = [&](int row, int c) {
-        return stage + row * (CH * 16) + ((CH == 8 ? c ^ (row & 7) : c ^ ((row >> 1) & 3)) << 4);
-    };
-    __syncwarp();
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]),
+                 "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+                 : "memory");
+}
+
+// N values as 16-bit elements of a row; wide: every row starts on 32 bytes (else on 16).
+template <typename T, int N>
+__device__ __forceinline__ void store_row(T *p, const float *x, bool wide)
+{
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at(lane, c)), "r"(v[c].x), "r"(v[c].y), "r"(v[c].z),
-                     "r"(v[c].w)
-                     : "memory");
-    __syncwarp();
+    for (int i = 0; i < N; i += 16) {
+        uint32_t u[8];
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-        const int row = i * (32 / CH) + lane / CH, c = lane % CH;
-        uint4 u;
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-                     : "r"(at(row, c))
-                     : "memory");
-        if (row < n_rows) reinterpret_cast<uint4 *>(dst(row))[c] = u;
+        for (int e = 0; e < 8; ++e) u[e] = pack2(T(), x[i + 2 * e], x[i + 2 * e + 1]);
+        if (wide) {
+            store32(p + i, u);
+        } else {
+            reinterpret_cast<uint4 *>(p + i)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+            reinterpret_cast<uint4 *>(p + i)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+        }
     }
 }
 
-template <typename T>
-__device__ __forceinline__ uint4 pack8(const float *x)
+template <int N>
+__device__ __forceinline__ void store_row(float *p, const uint32_t *x)
 {
-    return make_uint4(pack2(T(), x[0], x[1]), pack2(T(), x[2], x[3]), pack2(T(), x[4], x[5]), pack2(T(), x[6], x[7]));
+#pragma unroll
+    for (int i = 0; i < N; i += 8) store32(p + i, x + i);
 }
 
-__device__ __forceinline__ uint4 bits4(const float *x)
+// One warp copies the keys of tile j (rows of a key list, if any) into a tile,
+// rows past the set's nk keys as zeros: their memory is never read.
+template <typename T, int D, int ROWS>
+__device__ __noinline__ void copy_keys(const int32_t *list, int nk, int j, const T *base, int64_t sn, uint32_t dst)
 {
-    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-}
-
-// Copies the 128 keys of tile j (rows of a key list, if any) into a tile, rows
-// past the set's nk keys as zeros: their memory is never read.
-template <typename T, int D, int THREADS>
-__device__ __forceinline__ void copy_keys(const int32_t *list, int nk, int j, const T *base, int64_t sn, uint32_t dst,
-                                          int tid)
-{
-    constexpr int CH = D / 8, RPI = THREADS / CH;
-    const int ch = tid % CH;
+    constexpr int CH = D / 8, RPI = 32 / CH;
+    const int lane = threadIdx.x & 31, ch = lane % CH;
 #pragma unroll 8
-    for (int i = tid / CH; i < 128; i += RPI) {
-        const int kj = j * 128 + i;
+    for (int i = lane / CH; i < ROWS; i += RPI) {
+        const int kj = j * ROWS + i;
         const bool ok = kj < nk;
         const int key = ok ? (list ? list[kj] : kj) : 0;
-        tc::cp_async16(dst + tile_off(i, ch, 128), base + key * sn + ch * 8, ok);
+        tc::cp_async16(dst + tile_off(i, ch, ROWS), base + key * sn + ch * 8, ok);
     }
+}
+
+// One warp fills a ring with the key tiles (of k or of v) of its CTA's items.
+template <typename T, int D, int ROWS, int NS, typename Decode>
+__device__ __forceinline__ void fill_keys(const CrossArgs &a, RingFill<NS> ring, const CUtensorMap *map, const void *src,
+                                          int64_t sB, int64_t sH, int64_t sN, uint32_t smem, int items, const Waiter &wait,
+                                          int where, const Decode &decode)
+{
+    bool ok = true;
+#pragma unroll 1
+    for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
+        const auto w = decode(item);
+        const T *base = static_cast<const T *>(src) + w.bk * sB + w.hk * sH;
+        const int32_t *list = a.idx ? a.idx + (int64_t)w.bk * a.M : nullptr;
+#pragma unroll 1
+        for (int j = w.t0; j < w.t1; ++j) {
+            if (!(ok = ring.acquire(wait, where))) break;
+            const uint32_t dst = smem + ring.slot * (ROWS * D * 2);
+            if (tma_keys<ROWS>(a, w.nk, j)) {
+                ring.template tma<D, ROWS>(dst, map, j * ROWS, w.hk, w.bk);
+            } else {
+                copy_keys<T, D, ROWS>(list, w.nk, j, base, sN, dst);
+                ring.issued();
+            }
+        }
+    }
+    ring.finish(!ok);
 }
 
 cudaError_t cross_fwd_configure();

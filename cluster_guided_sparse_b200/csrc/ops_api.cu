@@ -329,6 +329,9 @@ op::CrossArgs cross_sizes(const scope_tensor *q, const scope_tensor *k)
     const int rows = a.heads * a.N;
     a.pairs = a.fold ? (rows + 255) / 256 : a.heads * ((a.N + 255) / 256);
     a.tiles = a.fold ? (rows + 127) / 128 : a.heads * (padded / 128);
+    a.by_N = op::Div(a.N);
+    a.by_G = op::Div(a.G);
+    a.by_Hk = op::Div(a.Hk);
     return a;
 }
 
@@ -338,6 +341,9 @@ CrossLayout cross_layout(op::CrossArgs &a, int D, bool masked)
     const int64_t total = (int64_t)a.B * a.H * a.N;
     a.splits = op::cross_fwd_splits(a.sets, a.pairs, a.M, total, D, kSms);
     a.items = a.sets * a.splits * a.pairs;
+    a.by_per = op::Div((a.N + 255) / 256);
+    a.by_tiles = op::Div(a.pairs);
+    a.by_splits = op::Div(a.splits);
     size_t cur = 256;
     L.idx = take(cur, masked ? (size_t)a.Bk * a.M * 4 : 0);
     L.cnt = take(cur, masked ? (size_t)a.Bk * 4 : 0);
@@ -357,6 +363,10 @@ CrossBwdLayout cross_bwd_layout(op::CrossArgs &a, int D, bool masked)
     const int64_t total = (int64_t)a.B * a.H * a.N;
     a.dq_splits = op::cross_dq_splits(a.sets, a.tiles, a.M, total, D, kSms);
     a.dkv_splits = op::cross_dkv_splits(a.sets, a.tiles, a.M, D, kSms);
+    a.by_per = op::Div((a.N + 127) / 128);
+    a.by_tiles = op::Div(a.tiles);
+    a.by_splits = op::Div(a.dq_splits);
+    a.by_dkv_splits = op::Div(a.dkv_splits);
     size_t cur = 256;
     const size_t keys = masked ? (size_t)a.Bk * a.M * 4 : 0, rows = (size_t)a.sets * a.tiles * 128 * 4;
     L.idx = take(cur, keys);
@@ -375,6 +385,12 @@ CrossBwdLayout cross_bwd_layout(op::CrossArgs &a, int D, bool masked)
     return L;
 }
 
+// Every row of a tensor of 16-bit elements starts on 32 bytes.
+bool rows_on_32(const scope_tensor *t, const RowStrides &s)
+{
+    return !(((uintptr_t)t->ptr | (uintptr_t)(2 * ((t->B > 1 ? s.sB : 0) | (t->H > 1 ? s.sH : 0) | (t->N > 1 ? s.sN : 0)))) & 31);
+}
+
 void cross_tensors(op::CrossArgs &a, const scope_tensor *q, const scope_tensor *k, const scope_tensor *v,
                    const scope_tensor *o, const scope_keys *keys, float scale)
 {
@@ -387,11 +403,12 @@ void cross_tensors(op::CrossArgs &a, const scope_tensor *q, const scope_tensor *
     a.kv_len = keys ? keys->len : nullptr;
     a.scale = scale != 0.f ? scale : 1.f / std::sqrt((float)q->D);
     a.scale_log2 = a.scale * 1.4426950408889634f;
+    a.wide = rows_on_32(o, os);
 }
 
-// Tensor map of 128-row x 64-column boxes; false where TMA cannot address the
+// Tensor map of boxes of `rows` rows x 64 columns; false where TMA cannot address the
 // layout (a stride of 2^40 bytes or more).
-bool tile_map(CUtensorMap *m, const scope_tensor *t)
+bool tile_map(CUtensorMap *m, const scope_tensor *t, int rows)
 {
     using Encode = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
@@ -415,7 +432,7 @@ bool tile_map(CUtensorMap *m, const scope_tensor *t)
         strides[i] = (cuuint64_t)(ext[i] > 1 ? str[i] : t->D) * 2;
         if (strides[i] >= (cuuint64_t)1 << 40) return false;
     }
-    const cuuint32_t box[4] = {64, 128, 1, 1}, one[4] = {1, 1, 1, 1};
+    const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1}, one[4] = {1, 1, 1, 1};
     return encode(m, t->dtype == SCOPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, t->ptr,
                   dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -423,10 +440,11 @@ bool tile_map(CUtensorMap *m, const scope_tensor *t)
 
 // The maps that a call's kernels use; what has none is copied by threads.
 void cross_maps(op::CrossArgs &a, op::CrossMaps &m, const scope_tensor *q, const scope_tensor *k, const scope_tensor *v,
-                const scope_tensor *d)
+                const scope_tensor *d)  // d: do, in the backward pass
 {
-    a.tma_kv = a.M > 0 && !a.idx && tile_map(&m.k, k) && tile_map(&m.v, v);
-    a.tma_rows = !a.fold && a.N > 0 && tile_map(&m.q, q) && (!d || tile_map(&m.d, d));
+    const int keys = d ? 128 : op::kFwdKeys;
+    a.tma_kv = a.M > 0 && !a.idx && tile_map(&m.k, k, keys) && tile_map(&m.v, v, keys);
+    a.tma_rows = !a.fold && a.N > 0 && tile_map(&m.q, q, 128) && (!d || tile_map(&m.d, d, 128));
 }
 
 }  // namespace
@@ -507,6 +525,7 @@ extern "C" scope_status scope_cross_attn_backward(const scope_tensor *d_o, const
     a.dB = ds.sB; a.dH = ds.sH; a.dN = ds.sN;
     a.dq = dq->ptr;
     a.dqB = qs.sB; a.dqH = qs.sH; a.dqN = qs.sN;
+    a.wide = rows_on_32(dq, qs);
     a.lse = const_cast<float *>(lse);  // read only here
     char *ws = (char *)workspace;
     a.nlse = (float *)(ws + L.nlse);
