@@ -20,7 +20,8 @@
 // epilogue.  Q rows have two buffers for the same reason.
 //
 // Warp roles (416 threads):
-//   warps 0-3, 4-7  softmax and epilogue of row tile 0, 1 (one thread per row)
+//   warps 0-3, 4-7  softmax and epilogue of row tile 0, 1 (one thread per row); O
+//                   leaves by TMA through the item's Q buffer
 //   warps 8, 9, 10  Q, K, V rows by TMA, or cp.async where a tile's rows are not
 //                   in order (cross_common.cuh)
 //   warps 11, 12    tcgen05.mma issuers of row tile 0, 1; warp 11 owns the TMEM
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
-            mbar_init(&q_empty[i], 2);
+            mbar_init(&q_empty[i], 8);
             for (int b = 0; b < 2; ++b) {
                 mbar_init(&s_full[i][b], 1);
                 mbar_init(&p_full[i][b], 4);
@@ -158,6 +159,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_
             if (w.t0 == w.t1) continue;
             const int buf = qi & 1;
             if (qi >= 2 && !(ok = wait.warp(&q_empty[buf], ((qi >> 1) - 1) & 1, 0x40))) break;
+            fence_async_smem();  // O has gone through the buffer
             load_rows<T, D>(a, w.r, w.hk, w.r.nq > kTile ? 2 : 1, &m.q, a.q, a.qB, a.qH, a.qN, sQ + buf * 2 * TB,
                             &q_full[buf]);
             ++qi;
@@ -182,48 +184,47 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_
         const uint64_t dq = sw128_desc(sQ + t * TB, 16, 1024), dk = sw128_desc(sK, 16, 1024);
         const uint64_t dv = sw128_desc(sV, kFwdKeys * 128, 1024);
         const uint32_t tS = tmem + t * 256, tO = tS + 128;
-        FwdSteps front, back;  // steps whose S, whose PV is next; the front is two ahead
+        FwdSteps front;  // the step whose S is next, two ahead of the one whose PV is
+        constexpr uint32_t kStep = 1, kFirst = 2, kLast = 4, kHas = 8;  // of an item; kHas: has this row tile
+        uint32_t back = 0, mid = 0;                                     // the steps behind the front one; 0: none
         RingRead<NS> kr, vr;
         int ns = 0, np = 0, no = 0;  // of this row tile: S, PV issued, items done
-        bool ok = true, more = front.seek(a, blockIdx.x), work = more;
-        back = front;
-        int lead = 0;
+        bool ok, more = front.seek(a, blockIdx.x);
 #pragma unroll 1
-        while (ok && work) {
-            const bool pv = lead == 2 || !more;
-            if (pv) {  // O (+)= P V of the back step
+        while (more | (back | mid) != 0) {
+            if (back) {  // O (+)= P V
                 uint64_t *v = &v_full[vr.slot];
-                if (t < back.nt) {
+                if (back & kHas) {
                     const int b = np & 1;
                     if (!(ok = wait.all(&p_full[t][b], (np >> 1) & 1, 0x45, v, vr.use & 1, 0x47))) break;
                     // the previous item's epilogue has read O
-                    if (back.first && no > 0 && !(ok = wait.warp(&o_empty[t], (no - 1) & 1, 0x46))) break;
+                    if ((back & kFirst) && no > 0 && !(ok = wait.warp(&o_empty[t], (no - 1) & 1, 0x46))) break;
                     tc_fence_after();
                     const uint64_t bv = dv + (uint64_t)((vr.slot * KB) >> 4);
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < kFwdKeys / 16; ++k)
-                            mma_ts(tO, tS + b * 64 + k * 8, bv + (uint64_t)((k * 2048) >> 4), id_pv, !back.first || k > 0);
+                            mma_ts(tO, tS + b * 64 + k * 8, bv + (uint64_t)((k * 2048) >> 4), id_pv, !(back & kFirst) || k > 0);
                         mma_commit(&o_full[t][b]);
                         mma_commit(&v_empty[vr.slot]);
                     }
                     __syncwarp();
                     ++np;
-                    if (back.j + 1 == back.t1) ++no;
+                    if (back & kLast) ++no;
                 } else {
                     if (!(ok = wait.warp(v, vr.use & 1, 0x4f))) break;
                     if (lane == 0) mbar_arrive(&v_empty[vr.slot]);
                 }
                 vr.next();
-                work = back.next(a);
-            } else {
-                ++lead;
             }
-            if (more) {  // S = Q K^T of the front step
+            back = mid;
+            mid = 0;
+            if (more) {  // S = Q K^T
                 const int buf = front.seq & 1;
-                const bool last = front.j + 1 == front.t1;
                 if (!(ok = wait.all(&k_full[kr.slot], kr.use & 1, 0x44, &q_full[buf], (front.seq >> 1) & 1, 0x43))) break;
+                mid = kStep | (front.first ? kFirst : 0) | (front.j + 1 == front.t1 ? kLast : 0);
                 if (t < front.nt) {
+                    mid |= kHas;
                     tc_fence_after();
                     const uint64_t aq = dq + (uint64_t)((buf * 2 * TB) >> 4), bk = dk + (uint64_t)((kr.slot * KB) >> 4);
                     const int b = ns & 1;
@@ -234,13 +235,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_
                                    bk + (uint64_t)(((k >> 2) * (kFwdKeys * 128) + (k & 3) * 32) >> 4), id_qk, k > 0);
                         mma_commit(&s_full[t][b]);
                         mma_commit(&k_empty[kr.slot]);
-                        if (last) mma_commit(&q_empty[buf]);
                     }
                     __syncwarp();
                     ++ns;
                 } else if (lane == 0) {
                     mbar_arrive(&k_empty[kr.slot]);
-                    if (last) mbar_arrive(&q_empty[buf]);
                 }
                 kr.next();
                 more = front.next(a);
@@ -251,16 +250,30 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_
         const int t = warp >> 2, wq = warp & 3;
         const uint32_t tT = tmem + ((uint32_t)(wq * 32) << 16) + t * 256, tO = tT + 128;
         const uint64_t scp = f2pack(a.scale_log2, a.scale_log2);
-        int ns = 0;
-        bool ok = true;
+        int ns = 0, qi = 0;
+        bool ok = true, leaving = false;  // leaving: the last item's O may still be on its way out of the Q buffer
+        auto q_free = [&]() {             // of the item before qi's
+            if (lane == 0) {
+                stored();
+                mbar_arrive(&q_empty[(qi & 1) ^ 1]);
+            }
+            leaving = false;
+        };
         FwdItem w = fwd_item(a, blockIdx.x);
 #pragma unroll 1
         for (int item = blockIdx.x; ok && item < a.items; item += gridDim.x) {
-            if (w.r.nq <= t * kTile) {  // no rows here
+            const bool some = w.t0 < w.t1;  // uniform for the CTA
+            const int buf = qi & 1;
+            if (w.r.nq <= t * kTile) {  // no rows here: the item's Q is free, once it has come
+                if (some) {
+                    if (leaving) q_free();
+                    if (!(ok = wait.warp(&q_full[buf], (qi >> 1) & 1, 0x4c))) break;
+                    if (lane == 0) mbar_arrive(&q_empty[buf]);
+                    ++qi;
+                }
                 w = fwd_item(a, item + gridDim.x);
                 continue;
             }
-            const bool some = w.t0 < w.t1;
             float m_run = -INFINITY;
             uint64_t lA = 0ull, lB = 0ull;
 #pragma unroll 1
@@ -330,6 +343,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[t][ns & 1]);
+                if (leaving) q_free();
             }
             if (!ok) break;
             float la, lb, lc, ld;
@@ -349,32 +363,49 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_
                 if (a.splits > 1) a.part_lse[part] = lse2;
                 else if (a.lse) a.lse[flat] = lse2 * 0.6931471805599453f;
             }
-            w = fwd_item(a, item + gridDim.x);  // while the last products run
+            const bool boxes = a.tma_o && a.splits == 1;
+            const int first = t * kTile + wq * 32, bh = w.r.h, bb = w.r.b, bn = w.r.n + first;
+            const bool rows = first < w.r.nq;            // uniform for the warp
+            w = fwd_item(a, item + gridDim.x);           // while the last products run
             if (some) {
                 if (!(ok = wait.warp(&o_full[t][(ns - 1) & 1], ((ns - 1) >> 1) & 1, 0x4a + t))) break;
                 tc_fence_after();
             }
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t r[32];
+            for (int c = 0; c < D / 64; ++c) {
+                uint32_t r[64];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) r[i] = 0u;
+                for (int i = 0; i < 64; ++i) r[i] = 0u;
                 if (some) {
-                    tmem_ld32(tO + c * 32, r);
+                    tmem_ld32(tO + c * 64, r);
+                    tmem_ld32(tO + c * 64 + 32, r + 32);
                     tmem_wait_ld();
-                    if (c == D / 32 - 1) {
+                    if (c == D / 64 - 1) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&o_empty[t]);
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * inv);
-                if (!store) continue;
-                if (a.splits > 1) store_row<32>(po + c * 32, r);
-                else store_row<T, 32>(o + c * 32, reinterpret_cast<const float *>(r), a.wide);
+                for (int i = 0; i < 64; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * inv);
+                const float *f = reinterpret_cast<const float *>(r);
+                if (boxes && some) {
+                    uint4 u[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) u[i] = pack8<T>(f + 8 * i);
+                    if (rows) store_box(sQ + (buf * 2 + t) * TB + c * (kTile * 128) + wq * (32 * 128), u, &m.o, c * 64, bn, bh, bb);
+                } else if (store) {
+                    if (a.splits > 1) store_row<64>(po + c * 64, r);
+                    else store_row<T, 64>(o + c * 64, f, a.wide);
+                }
+            }
+            if (some) {
+                ++qi;
+                leaving = true;
             }
         }
+        if (leaving && lane == 0) stored();
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();

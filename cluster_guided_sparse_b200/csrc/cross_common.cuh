@@ -21,7 +21,9 @@ namespace scope {
 namespace op {
 
 struct CrossMaps {
-    CUtensorMap q, k, v, d;  // [B][H][N][D] boxes of 128 (forward k, v: kFwdKeys) rows x 64 columns, 128B swizzle
+    // [B][H][N][D] boxes of 128 (forward k, v: kFwdKeys; o, in the backward pass dq: 32) rows x 64 columns, 128B
+    // swizzle
+    CUtensorMap q, k, v, d, o;
 };
 
 constexpr int kFwdKeys = 64;  // keys of a tile of the forward kernel
@@ -60,7 +62,7 @@ struct CrossArgs {
     int heads;                 // heads whose rows read one key set: G, or B * G
     int fold;                  // how rows are cut into tiles
     int wide;                  // rows of o (backward: dq) start on 32 bytes
-    int tma_kv, tma_rows;      // whether the k, v maps are valid, and the q, d ones (by head only)
+    int tma_kv, tma_rows, tma_o;  // whether the k, v maps are valid, and the q, d and o ones (by head only)
     int sets;                  // Bk * Hk
     int pairs, splits;         // 256-row tiles per set, key ranges (forward)
     // per: row tiles of a head; tiles, splits: of the forward's, of the dq kernel's items
@@ -354,9 +356,41 @@ __device__ __forceinline__ bool tma_keys(const CrossArgs &a, int nk, int j)
     return a.tma_kv && !a.idx && (nk == a.M || nk - j * ROWS >= ROWS);
 }
 
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float *x)
+{
+    return make_uint4(pack2(T(), x[0], x[1]), pack2(T(), x[2], x[3]), pack2(T(), x[4], x[5]), pack2(T(), x[6], x[7]));
+}
+
+// One warp's 32 rows x 64 columns of 16-bit values, this lane's row as 8 chunks,
+// into its part of a swizzled tile and from there to rows [n, n + 32) of head
+// (b, h) by TMA, which drops rows past the head's end.  The tile may be written
+// again after stored().  (Rows of 256 bytes straight from registers, 32 bytes a
+// thread and store, keep the load/store unit at one line a clock: 3000 clocks for
+// an item's 64 KB.)
+__device__ __forceinline__ void store_box(uint32_t smem, const uint4 *u, const CUtensorMap *m, int x, int n, int h, int b)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(smem + lane * 128 + ((c ^ (lane & 7)) << 4)),
+                     "r"(u[c].x), "r"(u[c].y), "r"(u[c].z), "r"(u[c].w)
+                     : "memory");
+    tc::fence_async_smem();
+    __syncwarp();
+    if (lane == 0)
+        asm volatile(
+            "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];\n\t"
+            "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(m)),
+            "r"(smem), "r"(x), "r"(n), "r"(h), "r"(b)
+            : "memory");
+}
+
+// This thread's store_box copies have left shared memory.
+__device__ __forceinline__ void stored() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
 // 16 values to 32 bytes of 16-bit elements, 8 to 32 bytes of fp32: whole sectors
-// of a row from one thread.  (Rows that go through shared memory leave in longer
-// segments, but the tensor cores keep it busy: 3100 clocks a 128-row tile.)
+// of a row from one thread.
 __device__ __forceinline__ void store32(void *p, const uint32_t *u)
 {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(u[0]), "r"(u[1]), "r"(u[2]),

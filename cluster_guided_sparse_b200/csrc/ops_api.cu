@@ -439,12 +439,14 @@ bool tile_map(CUtensorMap *m, const scope_tensor *t, int rows)
 }
 
 // The maps that a call's kernels use; what has none is copied by threads.
+// d: do, in the backward pass; o: what the rows' kernel writes, o or dq.
 void cross_maps(op::CrossArgs &a, op::CrossMaps &m, const scope_tensor *q, const scope_tensor *k, const scope_tensor *v,
-                const scope_tensor *d)  // d: do, in the backward pass
+                const scope_tensor *d, const scope_tensor *o)
 {
     const int keys = d ? 128 : op::kFwdKeys;
     a.tma_kv = a.M > 0 && !a.idx && tile_map(&m.k, k, keys) && tile_map(&m.v, v, keys);
     a.tma_rows = !a.fold && a.N > 0 && tile_map(&m.q, q, 128) && (!d || tile_map(&m.d, d, 128));
+    a.tma_o = !a.fold && a.N > 0 && tile_map(&m.o, o, 32);
 }
 
 }  // namespace
@@ -485,7 +487,7 @@ extern "C" scope_status scope_cross_attn(const scope_tensor *q, const scope_tens
         a.cnt = cnt;
     }
     op::CrossMaps m;
-    cross_maps(a, m, q, k, v, nullptr);
+    cross_maps(a, m, q, k, v, nullptr, o);
     op::launch_cross_fwd(a, m, (int)q->D, q->dtype == SCOPE_F16, kSms, s);
     return launch_status("scope_cross_attn");
 }
@@ -549,7 +551,7 @@ extern "C" scope_status scope_cross_attn_backward(const scope_tensor *d_o, const
     a.dv = dv->ptr;
     a.dvB = vs.sB; a.dvH = vs.sH; a.dvN = vs.sN;
     op::CrossMaps m;
-    cross_maps(a, m, q, k, v, d_o);
+    cross_maps(a, m, q, k, v, d_o, dq);
     op::launch_cross_bwd(a, m, (int)q->D, q->dtype == SCOPE_F16, kSms, inv, s);
     return launch_status("scope_cross_attn_backward");
 }
