@@ -169,12 +169,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_
     } else if (warp == 9 || warp == 10) {
         // ------------------------------------------------------------ K rows, V rows
         auto decode = [&](int item) { return fwd_item(a, item); };
+        auto any_time = [](int) { return true; };
         if (warp == 9)
             fill_keys<T, D, kFwdKeys>(a, RingFill<NS>(k_full, k_empty), &m.k, a.k, a.kB, a.kH, a.kN, sK, a.items, wait,
-                                      0x41, decode);
+                                      0x41, decode, any_time);
         else
             fill_keys<T, D, kFwdKeys>(a, RingFill<NS>(v_full, v_empty), &m.v, a.v, a.vB, a.vH, a.vN, sV, a.items, wait,
-                                      0x42, decode);
+                                      0x42, decode, any_time);
     } else if (warp >= 11) {
         // ------------------------------------------------------------ MMA issuer of row tile t
         // The whole warp runs the steps, so their values are uniform, and one lane issues (where a single lane ran

@@ -171,6 +171,7 @@ __device__ __noinline__ DqItem dq_item(const CrossArgs &a, int item)
 {
     DqItem w;
     int rt;
+    item = min(item, a.sets * a.dq_splits * a.tiles - 1);  // behind the last one any
     const int set = a.by_splits(a.by_tiles(item, rt), w.split);
     w.bk = a.by_Hk(set, w.hk);
     w.r = row_tile<kT>(a, w.bk, w.hk, rt);
@@ -202,7 +203,7 @@ struct DqStep {
 
 // One persistent CTA per SM; item = 128 rows of a key set and a key range.  TMEM:
 // X0 [0,128), X1 [128,256), sum t k [256,256+D), sum p k [384,384+D).  Shared
-// memory: 2 Q tiles (the next item's comes early), 1 dO
+// memory: 2 Q tiles (the next item's comes early; dq leaves through it), 1 dO
 // tile, rings of 3 K and 1 V tiles.  Warps 0-3 take the keys 0-63 of a tile,
 // warps 4-7 the keys 64-127, one thread per row and half; warps 8, 9, 10 load
 // Q and dO, K, V; warp 11 issues.
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.q_full[i], 1);
-            mbar_init(&bar.q_empty[i], 1);
+            mbar_init(&bar.q_empty[i], 8);
         }
         for (int i = 0; i < 3; ++i) {
             mbar_init(&bar.k_full[i], 1);
@@ -263,6 +264,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             if (w.t0 == w.t1) continue;
             const int buf = qi & 1;
             if (qi >= 2 && !(ok = wait.warp(&bar.q_empty[buf], ((qi >> 1) - 1) & 1, 0x50))) break;
+            fence_async_smem();  // dq has gone through the buffer
             load_rows<T, D>(a, w.r, w.hk, 1, &m.q, a.q, a.qB, a.qH, a.qN, sQ + buf * TB, &bar.q_full[buf]);
             ++qi;
             if (qi >= 2 && !(ok = wait.warp(&bar.o_empty, (qi - 2) & 1, 0x50))) break;
@@ -277,10 +279,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         auto decode = [&](int item) { return dq_item(a, item); };
         if (warp == 9)
             fill_keys<T, D, kT>(a, RingFill<3>(bar.k_full, bar.k_empty), &m.k, a.k, a.kB, a.kH, a.kN, sK, items, wait, 0x51,
-                                decode);
+                                decode, [](int) { return true; });
         else
             fill_keys<T, D, kT>(a, RingFill<1>(&bar.v_full, &bar.v_empty), &m.v, a.v, a.vB, a.vH, a.vN, sV, items, wait,
-                                0x5c, decode);
+                                0x5c, decode,
+                                // not while S(n) is computed, which takes shared memory's full rate
+                                [&](int n) { return n == 0 || wait.warp(&bar.s_full, n & 1, 0x5d); });
     } else if (warp == 11) {
         // ------------------------------------------------------------ MMA issuer
         // (by the whole warp, one lane issuing, as in cross_attn.cu)
@@ -295,11 +299,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             if (!wait.warp(&bar.k_full[slot], kr.use & 1, 0x53)) return false;
             kr.next();
             tc_fence_after();
-            const bool last = st.j + 1 == st.t1;
             if (elect_one()) {
                 tile_product<T, D>(tmem + (step & 1) * 128, sQ + (item & 1) * TB, sK + slot * TB);
                 mma_commit(&bar.s_full);
-                if (last) mma_commit(&bar.q_empty[item & 1]);
             }
             __syncwarp();
             return true;
@@ -347,12 +349,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int half = warp >> 2, wq = warp & 3, row = wq * 32 + lane;
         const uint32_t lane_off = (uint32_t)(wq * 32) << 16;
         int ns = 0, qi = 0;
-        bool ok = true;
+        bool ok = true, leaving = false;  // leaving: the last item's dq may still be on its way out of the Q buffer
+        auto q_free = [&]() {             // of the item before qi's
+            if (lane == 0) {
+                stored();
+                mbar_arrive(&bar.q_empty[(qi & 1) ^ 1]);
+            }
+            leaving = false;
+        };
         const uint64_t scp = f2pack(a.scale_log2, a.scale_log2);
+        DqItem w = dq_item(a, blockIdx.x);
+        float nl = a.nlse[w.at + row], nd = a.ndelta[w.at + row];
 #pragma unroll 1
         for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
-            const DqItem w = dq_item(a, item);
-            const float nl = a.nlse[w.at + row], nd = a.ndelta[w.at + row];
             const uint64_t nlp = f2pack(nl, nl), ndp = f2pack(nd, nd);
             uint64_t dA = 0ull, dB = 0ull;
 #pragma unroll 1
@@ -404,6 +413,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.ds_full);
+                if (leaving) q_free();
             }
             if (!ok) break;
             const bool store = row < w.r.nq;
@@ -426,6 +436,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     }
                     if (a.dq_splits > 1 && half == 0) a.part_delta[part] = 0.f;
                 }
+                w = dq_item(a, item + gridDim.x);
+                nl = a.nlse[w.at + row];
+                nd = a.ndelta[w.at + row];
                 continue;
             }
             // D - D' of the row: both halves' sums
@@ -448,6 +461,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     a.ndelta[w.at + row] = nd - delta;
                 }
             }
+            const int bh = w.r.h, bb = w.r.b, bn = w.r.n + wq * 32;
+            const bool rows = wq * 32 < w.r.nq;  // uniform for the warp
+            // the next item's values while the last products run
+            w = dq_item(a, item + gridDim.x);
+            nl = a.nlse[w.at + row];
+            nd = a.ndelta[w.at + row];
             if (!(ok = wait.warp(&bar.dq_full, qi & 1, 0x5b))) break;
             tc_fence_after();
             if (a.dq_splits > 1) {
@@ -460,6 +479,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     if (store) store_row<32>((e ? pe : pt) + c * 32, r);
                 }
             } else {
+                uint4 u[D / 16];
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
                     uint32_t r[32], e[32];
@@ -470,12 +490,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         f[i] = fmaf(-delta, __uint_as_float(e[i]), __uint_as_float(r[i])) * a.scale;
-                    if (store) store_row<T, 32>(dq + c * 32, f, a.wide);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) u[c * 4 + i] = pack8<T>(f + 8 * i);
+                    // a half row is one box's 64 columns at D = 128
+                    if ((D == 64 || !a.tma_o) && store) store_row<T, 32>(dq + c * 32, f, a.wide);
+                }
+                if constexpr (D == 128) {
+                    if (a.tma_o && rows)
+                        store_box(sQ + (qi & 1) * TB + half * (TB / 2) + wq * (32 * 128), u, &m.o, half * 64, bn, bh, bb);
                 }
             }
             tc_fence_before();
             ++qi;
+            leaving = true;
         }
+        if (leaving && lane == 0) stored();
+        __syncwarp();
     }
     bwd_epilogue(warp, tmem);
 }

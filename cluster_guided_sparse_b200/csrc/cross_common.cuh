@@ -439,13 +439,15 @@ __device__ __noinline__ void copy_keys(const int32_t *list, int nk, int j, const
     }
 }
 
-// One warp fills a ring with the key tiles (of k or of v) of its CTA's items.
-template <typename T, int D, int ROWS, int NS, typename Decode>
+// One warp fills a ring with the key tiles (of k or of v) of its CTA's items;
+// `before(n)` waits for what the n-th copy is to come after.
+template <typename T, int D, int ROWS, int NS, typename Decode, typename Before>
 __device__ __forceinline__ void fill_keys(const CrossArgs &a, RingFill<NS> ring, const CUtensorMap *map, const void *src,
                                           int64_t sB, int64_t sH, int64_t sN, uint32_t smem, int items, const Waiter &wait,
-                                          int where, const Decode &decode)
+                                          int where, const Decode &decode, const Before &before)
 {
     bool ok = true;
+    int n = 0;
 #pragma unroll 1
     for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
         const auto w = decode(item);
@@ -453,7 +455,7 @@ __device__ __forceinline__ void fill_keys(const CrossArgs &a, RingFill<NS> ring,
         const int32_t *list = a.idx ? a.idx + (int64_t)w.bk * a.M : nullptr;
 #pragma unroll 1
         for (int j = w.t0; j < w.t1; ++j) {
-            if (!(ok = ring.acquire(wait, where))) break;
+            if (!(ok = ring.acquire(wait, where) && before(n++))) break;
             const uint32_t dst = smem + ring.slot * (ROWS * D * 2);
             if (tma_keys<ROWS>(a, w.nk, j)) {
                 ring.template tma<D, ROWS>(dst, map, j * ROWS, w.hk, w.bk);
