@@ -291,23 +291,26 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         RingRead<3> kr;
         DqStep cur, nxt;
         int ns = 0, qi = 0;  // steps, items begun
-        auto issue_s = [&](const DqStep &st, int step, int &slot) {
-            if (st.j == st.t0) ++qi;
-            const int item = qi - 1;
-            if (!wait.warp(&bar.q_full[item & 1], (item >> 1) & 1, 0x52)) return false;
+        // S of a step has its operands (looked at early: each ready wait takes as long as an instruction's product)
+        auto s_ready = [&](const DqStep &st) {
+            if (st.j == st.t0) {
+                ++qi;
+                if (!wait.warp(&bar.q_full[(qi - 1) & 1], ((qi - 1) >> 1) & 1, 0x52)) return false;
+            }
+            return wait.warp(&bar.k_full[kr.slot], kr.use & 1, 0x53);
+        };
+        auto issue_s = [&](int step, int &slot) {
             slot = kr.slot;
-            if (!wait.warp(&bar.k_full[slot], kr.use & 1, 0x53)) return false;
             kr.next();
             tc_fence_after();
             if (elect_one()) {
-                tile_product<T, D>(tmem + (step & 1) * 128, sQ + (item & 1) * TB, sK + slot * TB);
+                tile_product<T, D>(tmem + (step & 1) * 128, sQ + ((qi - 1) & 1) * TB, sK + slot * TB);
                 mma_commit(&bar.s_full);
             }
             __syncwarp();
-            return true;
         };
         auto issue_dp = [&](const DqStep &st, int step) {
-            if (!wait.warp(&bar.o_full, (qi - 1) & 1, 0x54) || !wait.warp(&bar.v_full, step & 1, 0x55)) return false;
+            if (!wait.all(&bar.o_full, (qi - 1) & 1, 0x54, &bar.v_full, step & 1, 0x55)) return false;
             tc_fence_after();
             const bool last = st.j + 1 == st.t1;
             if (elect_one()) {
@@ -320,18 +323,25 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             return true;
         };
         int ks = 0, kn = 0;
-        bool more = cur.seek(a, blockIdx.x, items);
-        bool ok = more && issue_s(cur, 0, ks) && issue_dp(cur, 0);
+        bool more = cur.seek(a, blockIdx.x, items), ok = more && s_ready(cur);
+        if (ok) {
+            issue_s(0, ks);
+            ok = issue_dp(cur, 0);
+        }
 #pragma unroll 1
         while (ok && more) {
             nxt = cur;
             more = nxt.next(a, items);
-            // dP of this step has been read: the buffer is free for the next S
-            if (more && !(ok = wait.warp(&bar.dp_read, ns & 1, 0x56) && issue_s(nxt, ns + 1, kn))) break;
+            const bool first = cur.j == cur.t0, last = cur.j + 1 == cur.t1;
+            // The next S is out before this step's ds is awaited; at an item's end, where the epilogue waits for the
+            // sums, after them.  dP of this step has been read: its buffer is free for that S.
+            if (more && !last) {
+                if (!(ok = s_ready(nxt) && wait.warp(&bar.dp_read, ns & 1, 0x56))) break;
+                issue_s(ns + 1, kn);
+            }
             if (!(ok = wait.warp(&bar.ds_full, ns & 1, 0x57))) break;
             tc_fence_after();
             const uint32_t p = tmem + (ns & 1) * 128;
-            const bool first = cur.j == cur.t0, last = cur.j + 1 == cur.t1;
             if (elect_one()) {
                 tile_accumulate<T, D>(tmem + 256, p + 32, sK + ks * TB, first);
                 tile_accumulate<T, D>(tmem + 384, p, sK + ks * TB, first);
@@ -339,6 +349,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 if (last) mma_commit(&bar.dq_full);
             }
             __syncwarp();
+            if (more && last) {
+                if (!(ok = s_ready(nxt) && wait.warp(&bar.dp_read, ns & 1, 0x56))) break;
+                issue_s(ns + 1, kn);
+            }
             if (more && !(ok = issue_dp(nxt, ns + 1))) break;
             cur = nxt;
             ks = kn;
@@ -416,6 +430,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 if (leaving) q_free();
             }
             if (!ok) break;
+            // D - D' of the row: both halves' sums
+            float delta = 0.f;
+            float *pair = s_delta + (qi & 1) * 2 * kT + row;
+            if (w.t0 < w.t1) {
+                float d0, d1, d2, d3;
+                f2unpack(dA, d0, d1);
+                f2unpack(dB, d2, d3);
+                pair[half * kT] = (d0 + d2) + (d1 + d3);
+                // two buffers in turn: a warp may be in the next item before its pair has read this one's (but not in
+                // the one after, whose dP waits for the pair's ds)
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.delta_full[wq]);
+            }
             const bool store = row < w.r.nq;
             int b, h, n;
             tile_row(a, w.r, w.hk, store ? row : 0, b, h, n);
@@ -441,17 +468,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 nd = a.ndelta[w.at + row];
                 continue;
             }
-            // D - D' of the row: both halves' sums
-            float d0, d1, d2, d3;
-            f2unpack(dA, d0, d1);
-            f2unpack(dB, d2, d3);
-            float delta = (d0 + d2) + (d1 + d3);
-            // two buffers in turn: a warp may be in the next item before its pair has read this one's (but not in
-            // the one after, whose dP waits for the pair's ds)
-            float *pair = s_delta + (qi & 1) * 2 * kT + row;
-            pair[half * kT] = delta;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.delta_full[wq]);
             if (!(ok = wait.warp(&bar.delta_full[wq], qi & 1, 0x5a))) break;
             delta = pair[0] + pair[kT];
             if (half == 0) {
@@ -644,9 +660,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         RingRead<3> qr;
         RingRead<2> dr;
         const int n = uniform(i1 - i0);
+        auto s_ready = [&]() { return wait.warp(&bar.q_full[qr.slot], qr.use & 1, 0x61); };
         auto issue_s = [&](int u, int &slot) {
             slot = qr.slot;
-            if (!wait.warp(&bar.q_full[slot], qr.use & 1, 0x61)) return false;
             qr.next();
             tc_fence_after();
             if (elect_one()) {
@@ -654,7 +670,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 mma_commit(&bar.s_full);
             }
             __syncwarp();
-            return true;
         };
         auto issue_dp = [&](int u, int &slot) {
             slot = dr.slot;
@@ -669,11 +684,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             return true;
         };
         int qs = 0, qn = 0, os = 0;
-        bool ok = wait.warp(&bar.kv_full, 0, 0x63) && issue_s(0, qs) && issue_dp(0, os);
+        bool ok = wait.warp(&bar.kv_full, 0, 0x63) && s_ready();
+        if (ok) {
+            issue_s(0, qs);
+            ok = issue_dp(0, os);
+        }
 #pragma unroll 1
         for (int u = 0; ok && u < n; ++u) {
             const bool more = u + 1 < n;
-            if (more && !(ok = wait.warp(&bar.dp_read, u & 1, 0x64) && issue_s(u + 1, qn))) break;
+            if (more) {
+                if (!(ok = s_ready() && wait.warp(&bar.dp_read, u & 1, 0x64))) break;
+                issue_s(u + 1, qn);
+            }
             if (!(ok = wait.warp(&bar.ds_full, u & 1, 0x65))) break;
             tc_fence_after();
             const uint32_t p = tmem + (u & 1) * 128;
@@ -702,7 +724,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const ulonglong2 *nd = reinterpret_cast<const ulonglong2 *>(s_nd + dr.slot * kT + half * 64);
             const uint32_t tS = tmem + lane_off + (u & 1) * 128 + half * 64;
             const uint32_t tP = tmem + lane_off + ((u & 1) ^ 1) * 128 + half * 64;
-            if (!(ok = wait.warp(&bar.q_full[qr.slot], qr.use & 1, 0x66) && wait.warp(&bar.s_full, u & 1, 0x67))) break;
+            if (!(ok = wait.all(&bar.q_full[qr.slot], qr.use & 1, 0x66, &bar.s_full, u & 1, 0x67))) break;
             qr.next();
             tc_fence_after();
             uint32_t r[64];
@@ -721,7 +743,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 r[4 * c + 3] = __float_as_uint(ex2(x1));
             }
             store_half<T>(tS, r);
-            if (!(ok = wait.warp(&bar.o_full[dr.slot], dr.use & 1, 0x68) && wait.warp(&bar.dp_full, u & 1, 0x69))) break;
+            if (!(ok = wait.all(&bar.o_full[dr.slot], dr.use & 1, 0x68, &bar.dp_full, u & 1, 0x69))) break;
             dr.next();
             tc_fence_after();
             uint32_t d[64];
