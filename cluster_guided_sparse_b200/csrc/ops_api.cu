@@ -120,10 +120,19 @@ scope_status check_weight(const scope_vector *w, const char *name, float eps)
     return SCOPE_OK;
 }
 
-op::RopeTurns rope_turns(const scope_params *p)
+// The last call's angles of this thread serve again where their parameters are the same: 64 powers take longer
+// than a small call's kernel.
+const op::RopeTurns &rope_turns(const scope_params *p)
 {
-    op::RopeTurns t{};
-    const int ds[3] = {p->d_t, p->d_h, p->d_w};
+    static thread_local op::RopeTurns t;
+    static thread_local int32_t ds[3];
+    static thread_local double theta = 0.0;  // never valid
+    if (theta == p->theta && ds[0] == p->d_t && ds[1] == p->d_h && ds[2] == p->d_w) return t;
+    theta = p->theta;
+    ds[0] = p->d_t;
+    ds[1] = p->d_h;
+    ds[2] = p->d_w;
+    t = op::RopeTurns{};
     t.pt = p->d_t / 2;
     t.ph = p->d_h / 2;
     int at = 0;
