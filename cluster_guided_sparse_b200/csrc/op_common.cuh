@@ -42,6 +42,29 @@ __device__ __forceinline__ void load8(const __half *p, float *x)
     }
 }
 
+// The same in two steps: the bits, and later their values (half the registers of
+// a load in flight for 16-bit types).
+template <typename T>
+struct Raw8 {
+    uint4 u;
+    __device__ __forceinline__ void load(const T *p) { u = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void values(float *x) const { load8(reinterpret_cast<const T *>(&u), x); }
+};
+template <>
+struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p)
+    {
+        a = reinterpret_cast<const float4 *>(p)[0];
+        b = reinterpret_cast<const float4 *>(p)[1];
+    }
+    __device__ __forceinline__ void values(float *x) const
+    {
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+};
+
 __device__ __forceinline__ void store8(float *p, const float *x)
 {
     reinterpret_cast<float4 *>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
