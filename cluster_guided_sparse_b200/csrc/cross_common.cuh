@@ -58,6 +58,9 @@ struct CrossArgs {
     int64_t qB, qH, qN, kB, kH, kN, vB, vH, vN, oB, oH, oN;  // element strides
     const int32_t *kv_len;     // [Bk] or null: all M keys
     const int32_t *idx, *cnt;  // kept keys of a mask: [Bk][M] ascending, [Bk]; or null
+    const uint8_t *mask;       // the mask itself, [Bk][M] with mask_stride between rows (few rows), or null
+    int64_t mask_stride;
+    int few_ranks;             // CTAs of a key set where it has few rows (cross_few.cu), or 0
     int B, Bk, H, Hk, G, N, M;
     int heads;                 // heads whose rows read one key set: G, or B * G
     int fold;                  // how rows are cut into tiles
@@ -468,6 +471,9 @@ __device__ __forceinline__ void fill_keys(const CrossArgs &a, RingFill<NS> ring,
     ring.finish(!ok);
 }
 
+int cross_few_ranks(int64_t sets, int64_t rows, int64_t M, bool backward, int sms);
+void launch_cross_few(const CrossArgs &a, int D, bool f16, bool backward, cudaStream_t st);
+cudaError_t cross_few_configure();
 cudaError_t cross_fwd_configure();
 cudaError_t cross_bwd_configure();
 int cross_fwd_splits(int64_t sets, int64_t pairs, int64_t M, int64_t rows_total, int D, int sms);

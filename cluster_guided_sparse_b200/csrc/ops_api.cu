@@ -313,7 +313,8 @@ scope_status cross_ready()
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 64 && configured[dev]) return SCOPE_OK;
-    if (op::cross_fwd_configure() != cudaSuccess || op::cross_bwd_configure() != cudaSuccess)
+    if (op::cross_fwd_configure() != cudaSuccess || op::cross_bwd_configure() != cudaSuccess ||
+        op::cross_few_configure() != cudaSuccess)
         return fail(SCOPE_ECUDA, "kernel attribute setup failed");
     if (dev < 64) configured[dev] = true;
     return SCOPE_OK;
@@ -347,6 +348,9 @@ op::CrossArgs cross_sizes(const scope_tensor *q, const scope_tensor *k)
 CrossLayout cross_layout(op::CrossArgs &a, int D, bool masked)
 {
     CrossLayout L{};
+    L.total = 256;
+    a.few_ranks = op::cross_few_ranks(a.sets, (int64_t)a.heads * a.N, a.M, false, kSms);
+    if (a.few_ranks) return L;
     const int64_t total = (int64_t)a.B * a.H * a.N;
     a.splits = op::cross_fwd_splits(a.sets, a.pairs, a.M, total, D, kSms);
     a.items = a.sets * a.splits * a.pairs;
@@ -369,6 +373,9 @@ struct CrossBwdLayout {
 CrossBwdLayout cross_bwd_layout(op::CrossArgs &a, int D, bool masked)
 {
     CrossBwdLayout L{};
+    L.total = 256;
+    a.few_ranks = op::cross_few_ranks(a.sets, (int64_t)a.heads * a.N, a.M, true, kSms);
+    if (a.few_ranks) return L;
     const int64_t total = (int64_t)a.B * a.H * a.N;
     a.dq_splits = op::cross_dq_splits(a.sets, a.tiles, a.M, total, D, kSms);
     a.dkv_splits = op::cross_dkv_splits(a.sets, a.tiles, a.M, D, kSms);
@@ -410,6 +417,8 @@ void cross_tensors(op::CrossArgs &a, const scope_tensor *q, const scope_tensor *
     a.vB = vs.sB; a.vH = vs.sH; a.vN = vs.sN;
     a.oB = os.sB; a.oH = os.sH; a.oN = os.sN;
     a.kv_len = keys ? keys->len : nullptr;
+    a.mask = keys ? keys->mask : nullptr;
+    a.mask_stride = keys ? keys->mask_stride : 0;
     a.scale = scale != 0.f ? scale : 1.f / std::sqrt((float)q->D);
     a.scale_log2 = a.scale * 1.4426950408889634f;
     a.wide = rows_on_32(o, os);
@@ -489,6 +498,10 @@ extern "C" scope_status scope_cross_attn(const scope_tensor *q, const scope_tens
     a.part_o = (float *)(ws + L.part_o);
     a.part_lse = (float *)(ws + L.part_lse);
     cudaStream_t s = (cudaStream_t)stream;
+    if (a.few_ranks) {
+        op::launch_cross_few(a, (int)q->D, q->dtype == SCOPE_F16, false, s);
+        return launch_status("scope_cross_attn");
+    }
     if (masked) {
         int32_t *idx = (int32_t *)(ws + L.idx), *cnt = (int32_t *)(ws + L.cnt);
         op::launch_key_lists(keys->mask, keys->mask_stride, a.Bk, a.M, idx, cnt, nullptr, s);
@@ -546,7 +559,15 @@ extern "C" scope_status scope_cross_attn_backward(const scope_tensor *d_o, const
     a.part_delta = (float *)(ws + L.part_delta);
     a.part_dk = (float *)(ws + L.part_dk);
     a.part_dv = (float *)(ws + L.part_dv);
+    a.dk = dk->ptr;
+    a.dkB = ks.sB; a.dkH = ks.sH; a.dkN = ks.sN;
+    a.dv = dv->ptr;
+    a.dvB = vs.sB; a.dvH = vs.sH; a.dvN = vs.sN;
     cudaStream_t s = (cudaStream_t)stream;
+    if (a.few_ranks) {
+        op::launch_cross_few(a, (int)q->D, q->dtype == SCOPE_F16, true, s);
+        return launch_status("scope_cross_attn_backward");
+    }
     int32_t *inv = nullptr;
     if (masked) {
         int32_t *idx = (int32_t *)(ws + L.idx), *cnt = (int32_t *)(ws + L.cnt);
@@ -555,10 +576,6 @@ extern "C" scope_status scope_cross_attn_backward(const scope_tensor *d_o, const
         a.idx = idx;
         a.cnt = cnt;
     }
-    a.dk = dk->ptr;
-    a.dkB = ks.sB; a.dkH = ks.sH; a.dkN = ks.sN;
-    a.dv = dv->ptr;
-    a.dvB = vs.sB; a.dvH = vs.sH; a.dvN = vs.sN;
     op::CrossMaps m;
     cross_maps(a, m, q, k, v, d_o, dq);
     op::launch_cross_bwd(a, m, (int)q->D, q->dtype == SCOPE_F16, kSms, inv, s);
