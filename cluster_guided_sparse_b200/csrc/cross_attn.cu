@@ -61,7 +61,7 @@ struct FwdItem {
     RowTile r;
 };
 
-__device__ __noinline__ FwdItem fwd_item(const CrossArgs &a, int item)
+__device__ __forceinline__ FwdItem fwd_item(const CrossArgs &a, int item)
 {
     FwdItem w;
     int rt, set;

@@ -117,49 +117,6 @@ __device__ __forceinline__ void bwd_epilogue(int warp, uint32_t tmem)
     }
 }
 
-// nlse and ndelta (from the rounded o) of every row: one block per row tile.
-// Bound by HBM (o and do are read once).
-template <typename T, int D>
-__global__ void __launch_bounds__(256) cross_rows_kernel(const __grid_constant__ CrossArgs a)
-{
-    constexpr int LPR = D / 8, RPP = 256 / LPR;  // lanes a row, rows a pass
-    int rt, hk;
-    const int set = a.by_tiles((int)blockIdx.x, rt), bk = a.by_Hk(set, hk);
-    const RowTile w = row_tile<kT>(a, bk, hk, rt);
-    const int c8 = threadIdx.x % LPR, row0 = threadIdx.x / LPR;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        float sum[kT / RPP / 2], nl[kT / RPP / 2];
-#pragma unroll
-        for (int x = 0; x < kT / RPP / 2; ++x) {
-            const int i = (half * (kT / RPP / 2) + x) * RPP + row0;
-            sum[x] = 0.f;
-            nl[x] = -INFINITY;
-            if (i < w.nq) {
-                int b, h, n;
-                tile_row(a, w, hk, i, b, h, n);
-                float o[8], d[8];
-                load8(static_cast<const T *>(a.o) + b * a.oB + h * a.oH + n * a.oN + c8 * 8, o);
-                load8(static_cast<const T *>(a.dout) + b * a.dB + h * a.dH + n * a.dN + c8 * 8, d);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sum[x] = fmaf(o[e], d[e], sum[x]);
-                const float lse = a.lse[((int64_t)b * a.H + h) * a.N + n];
-                if (lse != -INFINITY) nl[x] = -lse * 1.4426950408889634f;
-            }
-        }
-#pragma unroll
-        for (int x = 0; x < kT / RPP / 2; ++x) {
-#pragma unroll
-            for (int o = LPR >> 1; o > 0; o >>= 1) sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], o);
-            if (c8 == 0) {
-                const int64_t at = (int64_t)blockIdx.x * kT + (half * (kT / RPP / 2) + x) * RPP + row0;
-                a.nlse[at] = nl[x];
-                a.ndelta[at] = -sum[x];
-            }
-        }
-    }
-}
-
 // ---------------------------------------------------------------- dq
 struct DqItem {
     int bk, hk, t0, t1, nk, split;
@@ -167,7 +124,7 @@ struct DqItem {
     RowTile r;
 };
 
-__device__ __noinline__ DqItem dq_item(const CrossArgs &a, int item)
+__device__ __forceinline__ DqItem dq_item(const CrossArgs &a, int item)
 {
     DqItem w;
     int rt;
@@ -179,6 +136,52 @@ __device__ __noinline__ DqItem dq_item(const CrossArgs &a, int item)
     w.nk = keys_of(a, w.bk);
     split_range((w.nk + kT - 1) / kT, w.split, a.by_splits, w.t0, w.t1);
     return w;
+}
+
+// -D' (do . o, of the rounded o) of 16 rows of a tile by each of eight warps, and
+// -lse in base 2 of this thread's own row: -inf, so that p is 0, where the row
+// reads nothing or does not exist.
+template <typename T, int D>
+__device__ __forceinline__ float row_values(const CrossArgs &a, RowTile w, int hk, float *s_nd)
+{
+    constexpr int LPR = D / 8, RPP = 32 / LPR, U = 16 / RPP;  // lanes a row, rows a pass, passes
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c8 = lane % LPR, row = (warp & 3) * 32 + lane;
+    Raw8<T> o[U], y[U];
+    int b, h, n;
+    // each lane's row address, handed round: 64-bit products for each row would take longer than the loads
+    const int mine = warp * 16 + (lane & 15);
+    tile_row(a, w, hk, min(mine, w.nq - 1), b, h, n);
+    const T *po = static_cast<const T *>(a.o) + b * a.oB + h * a.oH + n * a.oN;
+    const T *py = static_cast<const T *>(a.dout) + b * a.dB + h * a.dH + n * a.dN;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int from = u * RPP + lane / LPR;
+        const T *to = reinterpret_cast<const T *>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(po), from));
+        const T *ty = reinterpret_cast<const T *>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(py), from));
+        o[u].u = y[u].u = make_uint4(0u, 0u, 0u, 0u);
+        if (warp * 16 + from < w.nq) {
+            o[u].load(to + c8 * 8);
+            y[u].load(ty + c8 * 8);
+        }
+    }
+    float nl = -INFINITY;
+    if (row < w.nq) {
+        tile_row(a, w, hk, row, b, h, n);
+        const float lse = a.lse[((int64_t)b * a.H + h) * a.N + n];
+        if (lse != -INFINITY) nl = -lse * 1.4426950408889634f;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        float x[8], z[8], sum = 0.f;
+        o[u].values(x);
+        y[u].values(z);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum = fmaf(x[e], z[e], sum);
+#pragma unroll
+        for (int e = LPR >> 1; e > 0; e >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, e);
+        if (c8 == 0) s_nd[warp * 16 + u * RPP + lane / LPR] = -sum;
+    }
+    return nl;
 }
 
 // A CTA's key tiles in order, over its items; by a whole warp.
@@ -206,7 +209,11 @@ struct DqStep {
 // memory: 2 Q tiles (the next item's comes early; dq leaves through it), 1 dO
 // tile, rings of 3 K and 1 V tiles.  Warps 0-3 take the keys 0-63 of a tile,
 // warps 4-7 the keys 64-127, one thread per row and half; warps 8, 9, 10 load
-// Q and dO, K, V; warp 11 issues.
+// Q and dO, K, V; warp 11 issues.  The softmax warps compute the next item's D'
+// while this one waits for its sums: a launch of its own for them made 16 heads of
+// 2048 rows x 77 keys take 84 us instead of 74 with gradients, and 40 heads of
+// 32760 rows x 512 keys 1890 instead of 1927; one loader warp for all rows of an
+// item was three times too slow.
 template <typename T, int D>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     cross_dq_kernel(const __grid_constant__ CrossArgs a, const __grid_constant__ CrossMaps m, int items)
@@ -214,10 +221,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     constexpr int TB = kT * D * 2;
     const uint32_t sQ = smem_u32(smem_raw), sO = sQ + 2 * TB, sK = sQ + 3 * TB, sV = sQ + 6 * TB;
-    float *s_delta = reinterpret_cast<float *>(smem_raw + kTiles * TB);  // [2 items][2 halves][kT]
+    // [2 halves][kT] and, of items in turn, [2][kT].  Every warp announces the next item's D' after it has read this
+    // one's sums, and waits for all before it uses them, so neither is written before it has been read.
+    float *s_delta = reinterpret_cast<float *>(smem_raw + kTiles * TB), *s_nd = s_delta + 2 * kT;
     struct Barriers {
         uint64_t q_full[2], q_empty[2], o_full, o_empty, k_full[3], k_empty[3], v_full, v_empty;
-        uint64_t s_full, dp_full, dp_read, ds_full, dq_full, delta_full[4];
+        uint64_t s_full, dp_full, dp_read, ds_full, dq_full, delta_full[4], rows_full[2];
         uint32_t tmem_base;
         int abort;
     };
@@ -232,6 +241,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.q_full[i], 1);
             mbar_init(&bar.q_empty[i], 8);
+            mbar_init(&bar.rows_full[i], 8);
         }
         for (int i = 0; i < 3; ++i) {
             mbar_init(&bar.k_full[i], 1);
@@ -266,6 +276,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             if (qi >= 2 && !(ok = wait.warp(&bar.q_empty[buf], ((qi >> 1) - 1) & 1, 0x50))) break;
             fence_async_smem();  // dq has gone through the buffer
             load_rows<T, D>(a, w.r, w.hk, 1, &m.q, a.q, a.qB, a.qH, a.qN, sQ + buf * TB, &bar.q_full[buf]);
+#pragma unroll 1
+            for (int i = lane; i < w.r.nq; i += 32) {  // o and do will be read soon
+                int b, h, n;
+                tile_row(a, w.r, w.hk, i, b, h, n);
+                const T *o = static_cast<const T *>(a.o) + b * a.oB + h * a.oH + n * a.oN;
+                const T *y = static_cast<const T *>(a.dout) + b * a.dB + h * a.dH + n * a.dN;
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(o));
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(y));
+                if (D == 128) {
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(o + 64));
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(y + 64));
+                }
+            }
             ++qi;
             if (qi >= 2 && !(ok = wait.warp(&bar.o_empty, (qi - 2) & 1, 0x50))) break;
             load_rows<T, D>(a, w.r, w.hk, 1, &m.d, a.dout, a.dB, a.dH, a.dN, sO, &bar.o_full);
@@ -372,14 +395,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             leaving = false;
         };
         const uint64_t scp = f2pack(a.scale_log2, a.scale_log2);
-        DqItem w = dq_item(a, blockIdx.x);
-        float nl = a.nlse[w.at + row], nd = a.ndelta[w.at + row];
+        DqItem w{};
+        float nl = 0.f;
+        bool begun = false;  // w is an item, the one before `next`
 #pragma unroll 1
-        for (int item = blockIdx.x; ok && item < items; item += gridDim.x) {
+        for (int next = blockIdx.x;; next += gridDim.x) {
+            const bool keys = begun && w.t0 < w.t1;
+            float nd = 0.f, delta = 0.f;
+            if (keys) {
+                if (!(ok = wait.warp(&bar.rows_full[qi & 1], (qi >> 1) & 1, 0x5e))) break;
+                nd = s_nd[(qi & 1) * kT + row];
+            }
             const uint64_t nlp = f2pack(nl, nl), ndp = f2pack(nd, nd);
             uint64_t dA = 0ull, dB = 0ull;
 #pragma unroll 1
-            for (int j = w.t0; j < w.t1; ++j, ++ns) {
+            for (int j = w.t0; keys && j < w.t1; ++j, ++ns) {
                 const uint32_t tS = tmem + lane_off + (ns & 1) * 128 + half * 64;
                 const uint32_t tP = tmem + lane_off + ((ns & 1) ^ 1) * 128 + half * 64;
                 if (!(ok = wait.warp(&bar.s_full, ns & 1, 0x58))) break;
@@ -431,58 +461,63 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
             if (!ok) break;
             // D - D' of the row: both halves' sums
-            float delta = 0.f;
-            float *pair = s_delta + (qi & 1) * 2 * kT + row;
-            if (w.t0 < w.t1) {
+            float *pair = s_delta + row;
+            if (keys) {
                 float d0, d1, d2, d3;
                 f2unpack(dA, d0, d1);
                 f2unpack(dB, d2, d3);
                 pair[half * kT] = (d0 + d2) + (d1 + d3);
-                // two buffers in turn: a warp may be in the next item before its pair has read this one's (but not in
-                // the one after, whose dP waits for the pair's ds)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.delta_full[wq]);
             }
-            const bool store = row < w.r.nq;
+            const bool store = begun && row < w.r.nq;
             int b, h, n;
             tile_row(a, w.r, w.hk, store ? row : 0, b, h, n);
             const int64_t part = w.split * (int64_t)a.B * a.H * a.N + ((int64_t)b * a.H + h) * a.N + n;
             T *dq = static_cast<T *>(a.dq) + b * a.dqB + h * a.dqH + n * a.dqN + half * (D / 2);
             float *pt = a.part_t + part * D + half * (D / 2), *pe = a.part_e + part * D + half * (D / 2);
-            if (w.t0 == w.t1) {  // no keys
-                if (store) {
-                    const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-                    for (int i = 0; i < D / 2; i += 8) {
-                        if (a.dq_splits > 1) {
-                            store8(pt + i, zero);
-                            store8(pe + i, zero);
-                        } else {
-                            store8(dq + i, zero);
-                        }
+            if (keys) {
+                if (!(ok = wait.warp(&bar.delta_full[wq], qi & 1, 0x5a))) break;
+                delta = pair[0] + pair[kT];
+                // for the dk/dv kernel; of split keys the join takes the sum of the ranges' deltas off
+                if (half == 0) {
+                    if (a.dq_splits > 1 && store) a.part_delta[part] = delta;
+                    if (w.split == 0 || a.dq_splits == 1) {
+                        a.nlse[w.at + row] = nl;
+                        a.ndelta[w.at + row] = a.dq_splits > 1 ? nd : nd - delta;
                     }
-                    if (a.dq_splits > 1 && half == 0) a.part_delta[part] = 0.f;
                 }
-                w = dq_item(a, item + gridDim.x);
-                nl = a.nlse[w.at + row];
-                nd = a.ndelta[w.at + row];
-                continue;
-            }
-            if (!(ok = wait.warp(&bar.delta_full[wq], qi & 1, 0x5a))) break;
-            delta = pair[0] + pair[kT];
-            if (half == 0) {
-                if (a.dq_splits > 1) {
-                    if (store) a.part_delta[part] = delta;
-                } else {
-                    a.ndelta[w.at + row] = nd - delta;
+            } else if (store) {
+                const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                for (int i = 0; i < D / 2; i += 8) {
+                    if (a.dq_splits > 1) {
+                        store8(pt + i, zero);
+                        store8(pe + i, zero);
+                    } else {
+                        store8(dq + i, zero);
+                    }
                 }
+                if (a.dq_splits > 1 && half == 0) a.part_delta[part] = 0.f;
             }
             const int bh = w.r.h, bb = w.r.b, bn = w.r.n + wq * 32;
-            const bool rows = wq * 32 < w.r.nq;  // uniform for the warp
-            // the next item's values while the last products run
-            w = dq_item(a, item + gridDim.x);
-            nl = a.nlse[w.at + row];
-            nd = a.ndelta[w.at + row];
+            const bool rows = begun && wq * 32 < w.r.nq;  // uniform for the warp
+            // the next item's values while this one's last products run
+            const bool more = next < items;
+            begun = true;
+            if (more) {
+                w = dq_item(a, next);
+                if (w.t0 < w.t1) {
+                    const int to = (qi + (keys ? 1 : 0)) & 1;
+                    nl = row_values<T, D>(a, w.r, w.hk, s_nd + to * kT);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.rows_full[to]);
+                }
+            }
+            if (!keys) {
+                if (more) continue;
+                break;
+            }
             if (!(ok = wait.warp(&bar.dq_full, qi & 1, 0x5b))) break;
             tc_fence_after();
             if (a.dq_splits > 1) {
@@ -519,6 +554,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             tc_fence_before();
             ++qi;
             leaving = true;
+            if (!more) break;
         }
         if (leaving && lane == 0) stored();
         __syncwarp();
@@ -905,10 +941,9 @@ static void launch_bwd_t(const CrossArgs &a, const CrossMaps &m, int sms, const 
         count_launches(1);
         return;
     }
-    cross_rows_kernel<T, D><<<(unsigned)(a.sets * a.tiles), 256, 0, st>>>(a);
     const int dq_items = a.sets * a.dq_splits * a.tiles;
     cross_dq_kernel<T, D><<<dq_items < sms ? dq_items : sms, kBwdThreads, bwd_smem(D), st>>>(a, m, dq_items);
-    count_launches(2);
+    count_launches(1);
     if (a.dq_splits > 1) {
         const int64_t threads = (int64_t)a.B * a.H * a.N * (D / 8);
         cross_dq_join_kernel<T><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(a, D);
