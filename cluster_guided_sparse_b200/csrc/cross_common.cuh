@@ -87,7 +87,7 @@ struct CrossArgs {
     float *part_t, *part_e;    // [dq_splits][B*H*N][D] (dq_splits > 1)
     float *part_delta;         // [dq_splits][B*H*N]
     int dkv_splits;            // row ranges of the dk/dv kernel
-    float *part_dk, *part_dv;  // [dkv_splits][sets][M][D], kept keys in list order (dkv_splits > 1 or a list)
+    float *part_dk, *part_dv;  // [dkv_splits][sets][M][D], kept keys in list order
     void *dk, *dv;
     int64_t dkB, dkH, dkN, dvB, dvH, dvN;
 };
