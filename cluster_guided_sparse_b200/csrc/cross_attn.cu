@@ -108,6 +108,8 @@ struct FwdSteps {
 template <typename T, int D>
 __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_constant__ CrossArgs a, const __grid_constant__ CrossMaps m)
 {
+    wait_for_previous();
+    let_next_start();
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *sm = (unsigned char *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     constexpr int TB = kTile * D * 2, KB = kFwdKeys * D * 2;  // bytes of a row tile, of a key tile
@@ -425,6 +427,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_
 template <typename T>
 __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__ CrossArgs a, int D)
 {
+    wait_for_previous();
     const int lpr = D / 8;
     const int64_t total = (int64_t)a.B * a.H * a.N;
     const int64_t row = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / lpr;
@@ -457,6 +460,7 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
 __global__ void __launch_bounds__(1024) key_lists_kernel(const uint8_t *mask, int64_t stride, int M, int32_t *idx,
                                                          int32_t *cnt, int32_t *inv)
 {
+    let_next_start();
     __shared__ int tmp[33];
     const uint8_t *mk = mask + blockIdx.x * stride;
     int32_t *list = idx + (int64_t)blockIdx.x * M;
@@ -530,24 +534,32 @@ int cross_fwd_splits(int64_t sets, int64_t pairs, int64_t M, int64_t rows_total,
     return best;
 }
 
-template <typename T>
-static void launch_fwd_t(const CrossArgs &a, const CrossMaps &m, int D, int grid, cudaStream_t st)
+// The first kernel of a call is launched as any other: it follows whatever the stream holds.
+template <typename T, int D>
+static void launch_fwd_t(const CrossArgs &a, const CrossMaps &m, int grid, cudaStream_t st)
 {
-    if (D == 128) cross_fwd_kernel<T, 128><<<grid, kFwdThreads, fwd_smem(128), st>>>(a, m);
-    else cross_fwd_kernel<T, 64><<<grid, kFwdThreads, fwd_smem(64), st>>>(a, m);
-    count_launches(1);
+    if (a.idx) {
+        launch_next(cross_fwd_kernel<T, D>, grid, kFwdThreads, fwd_smem(D), st, a, m);
+    } else {
+        cross_fwd_kernel<T, D><<<grid, kFwdThreads, fwd_smem(D), st>>>(a, m);
+        count_launches(1);
+    }
     if (a.splits > 1) {
         const int64_t threads = (int64_t)a.B * a.H * a.N * (D / 8);
-        cross_join_kernel<T><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(a, D);
-        count_launches(1);
+        launch_next(cross_join_kernel<T>, (threads + 255) / 256, 256, 0, st, a, D);
     }
 }
 
 void launch_cross_fwd(const CrossArgs &a, const CrossMaps &m, int D, bool f16, int sms, cudaStream_t st)
 {
     const int grid = a.items < sms ? a.items : sms;
-    if (f16) launch_fwd_t<__half>(a, m, D, grid, st);
-    else launch_fwd_t<__nv_bfloat16>(a, m, D, grid, st);
+    if (f16) {
+        if (D == 128) launch_fwd_t<__half, 128>(a, m, grid, st);
+        else launch_fwd_t<__half, 64>(a, m, grid, st);
+    } else {
+        if (D == 128) launch_fwd_t<__nv_bfloat16, 128>(a, m, grid, st);
+        else launch_fwd_t<__nv_bfloat16, 64>(a, m, grid, st);
+    }
 }
 
 }  // namespace op

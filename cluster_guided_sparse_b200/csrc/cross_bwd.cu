@@ -222,6 +222,8 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     cross_dq_kernel(const __grid_constant__ CrossArgs a, const __grid_constant__ CrossMaps m, int items)
 {
+    wait_for_previous();
+    let_next_start();
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     constexpr int TB = kT * D * 2;
     const uint32_t sQ = smem_u32(smem_raw), sO = sQ + 2 * TB, sK = sQ + 3 * TB, sV = sQ + 6 * TB;
@@ -570,6 +572,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 template <typename T>
 __global__ void __launch_bounds__(256) cross_dq_join_kernel(const __grid_constant__ CrossArgs a, int D)
 {
+    wait_for_previous();
+    let_next_start();
     const int lpr = D / 8;
     const int64_t total = (int64_t)a.B * a.H * a.N;
     const int64_t row = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / lpr;
@@ -605,6 +609,8 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     cross_dkv_kernel(const __grid_constant__ CrossArgs a, const __grid_constant__ CrossMaps m, int key_tiles)
 {
+    wait_for_previous();
+    let_next_start();
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     constexpr int TB = kT * D * 2;
     const uint32_t sK = smem_u32(smem_raw), sV = sK + TB, sQ = sK + 2 * TB, sO = sK + 5 * TB;
@@ -851,6 +857,7 @@ template <typename T>
 __global__ void __launch_bounds__(256) cross_dkv_join_kernel(const __grid_constant__ CrossArgs a,
                                                              const int32_t *inv, int D)
 {
+    wait_for_previous();
     const int lpr = D / 8;
     const int64_t row = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / lpr;  // set * M + m
     const int c8 = threadIdx.x % lpr;
@@ -936,28 +943,29 @@ int cross_dkv_splits(int64_t sets, int64_t tiles, int64_t M, int D, int sms)
 template <typename T, int D>
 static void launch_bwd_t(const CrossArgs &a, const CrossMaps &m, int sms, const int32_t *inv, cudaStream_t st)
 {
-    const int64_t key_threads = (int64_t)a.sets * a.M * (D / 8);
-    const unsigned join_blocks = (unsigned)((key_threads + 255) / 256);
+    const int64_t join_blocks = ((int64_t)a.sets * a.M * (D / 8) + 255) / 256;
     if (a.N == 0) {  // no row: dk = dv = 0
         CrossArgs none = a;
         none.dkv_splits = 0;
-        cross_dkv_join_kernel<T><<<join_blocks, 256, 0, st>>>(none, inv, D);
+        cross_dkv_join_kernel<T><<<(unsigned)join_blocks, 256, 0, st>>>(none, inv, D);
         count_launches(1);
         return;
     }
-    const int dq_items = a.sets * a.dq_splits * a.tiles;
-    cross_dq_kernel<T, D><<<dq_items < sms ? dq_items : sms, kBwdThreads, bwd_smem(D), st>>>(a, m, dq_items);
-    count_launches(1);
+    const int dq_items = a.sets * a.dq_splits * a.tiles, dq_grid = dq_items < sms ? dq_items : sms;
+    if (a.idx) {  // after the key lists
+        launch_next(cross_dq_kernel<T, D>, dq_grid, kBwdThreads, bwd_smem(D), st, a, m, dq_items);
+    } else {
+        cross_dq_kernel<T, D><<<dq_grid, kBwdThreads, bwd_smem(D), st>>>(a, m, dq_items);
+        count_launches(1);
+    }
     if (a.dq_splits > 1) {
         const int64_t threads = (int64_t)a.B * a.H * a.N * (D / 8);
-        cross_dq_join_kernel<T><<<(unsigned)((threads + 255) / 256), 256, 0, st>>>(a, D);
-        count_launches(1);
+        launch_next(cross_dq_join_kernel<T>, (threads + 255) / 256, 256, 0, st, a, D);
     }
     if (a.M == 0) return;
     const int key_tiles = (a.M + kT - 1) / kT;
-    cross_dkv_kernel<T, D><<<(unsigned)(a.sets * a.dkv_splits * key_tiles), kBwdThreads, bwd_smem(D), st>>>(a, m, key_tiles);
-    cross_dkv_join_kernel<T><<<join_blocks, 256, 0, st>>>(a, inv, D);
-    count_launches(2);
+    launch_next(cross_dkv_kernel<T, D>, (int64_t)a.sets * a.dkv_splits * key_tiles, kBwdThreads, bwd_smem(D), st, a, m, key_tiles);
+    launch_next(cross_dkv_join_kernel<T>, join_blocks, 256, 0, st, a, inv, D);
 }
 
 void launch_cross_bwd(const CrossArgs &a, const CrossMaps &m, int D, bool f16, int sms, const int32_t *inv,

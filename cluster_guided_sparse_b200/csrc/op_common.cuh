@@ -94,6 +94,30 @@ __device__ __forceinline__ void store8(T *p, const float *x)
     *reinterpret_cast<uint4 *>(p) = u;
 }
 
+// ---------------------------------------------------------------- launches
+// The kernels of a call follow each other by programmatic launch: the next one's
+// blocks come to the SMs as this one's leave them, and wait before they read
+// anything until it has ended.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... Args, typename... Given>
+void launch_next(void (*kernel)(Args...), int64_t blocks, int threads, size_t smem, cudaStream_t st, const Given &...given)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, kernel, Args(given)...);
+    count_launches(1);
+}
+
 // ---------------------------------------------------------------- rotary positions (rope_op.cu)
 // Turns (1 = a full rotation) per unit of position of each pair of the head
 // dim; pairs [0, pt) belong to the t axis, [pt, pt + ph) to h, the rest to w.

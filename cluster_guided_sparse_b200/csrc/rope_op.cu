@@ -208,6 +208,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
     rope_op_bwd_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ RopeTurns t)
 {
     constexpr int D = LPR * 8, TPB = kRopeThreads / LPR, kB = sizeof(T) == 4 ? 2 : 4;
+    let_next_start();
     __shared__ float part[TPB][D];
     const int c8 = threadIdx.x % LPR;
     const int h0 = blockIdx.y * a.heads_per_block, h1 = min(a.H, h0 + a.heads_per_block);
@@ -294,6 +295,7 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
 // dw[d] = sum of the blocks' partial sums, in fp64; one block per 8 columns.
 __global__ void __launch_bounds__(512) rope_dw_kernel(const float *part, int parts, int D, void *dw, int w_dtype)
 {
+    wait_for_previous();
     __shared__ double acc[64][8];
     const int c = threadIdx.x & 7, g = threadIdx.x >> 3, d = blockIdx.x * 8 + c;
     double s = 0.0;
@@ -380,8 +382,8 @@ void launch_rope_op_bwd(RopeArgs a, const RopeTurns &t, int dtype, void *dw, cud
     if (dtype == SCOPE_F32) launch_bwd_t<float>(a, t, grid, st);
     else if (dtype == SCOPE_BF16) launch_bwd_t<__nv_bfloat16>(a, t, grid, st);
     else launch_bwd_t<__half>(a, t, grid, st);
-    rope_dw_kernel<<<a.D / 8, 512, 0, st>>>(a.dw_part, (int)(grid.x * grid.y), a.D, dw, a.w_dtype);
-    count_launches(2);
+    count_launches(1);
+    launch_next(rope_dw_kernel, a.D / 8, 512, 0, st, a.dw_part, (int)(grid.x * grid.y), a.D, dw, a.w_dtype);
 }
 
 }  // namespace op
