@@ -20,7 +20,9 @@
 // kernel therefore sums t_ij = p_ij (dp_ij - D'_i), which sum to D_i - D'_i over
 // a row (held in fp32), next to E_i = sum_j p_ij k_j, and takes
 //   dq_i = scale (sum_j t_ij k_j - (D_i - D'_i) E_i),
-// and the dk/dv kernel after it reads the corrected D_i.
+// and the dk/dv kernel after it reads the corrected D_i.  Where a row reads a
+// single key, p is 1 whatever its score, and dq, dk are set to 0 instead of to
+// what the roundings of t leave.
 //
 // Both run the same pipeline over two TMEM buffers X0, X1 of 128 columns: S of
 // step i goes to X[i%2], dP to the other; p and ds (16 bit, 64 columns each)
@@ -506,6 +508,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 }
                 if (a.dq_splits > 1 && half == 0) a.part_delta[part] = 0.f;
             }
+            const float scale = w.nk == 1 ? 0.f : a.scale;
             const int bh = w.r.h, bb = w.r.b, bn = w.r.n + wq * 32;
             const bool rows = begun && wq * 32 < w.r.nq;  // uniform for the warp
             // the next item's values while this one's last products run
@@ -546,7 +549,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     float f[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        f[i] = fmaf(-delta, __uint_as_float(e[i]), __uint_as_float(r[i])) * a.scale;
+                        f[i] = fmaf(-delta, __uint_as_float(e[i]), __uint_as_float(r[i])) * scale;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) u[c * 4 + i] = pack8<T>(f + 8 * i);
                     // a half row is one box's 64 columns at D = 128
@@ -592,9 +595,10 @@ __global__ void __launch_bounds__(256) cross_dq_join_kernel(const __grid_constan
             e[i] += y[i];
         }
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = fmaf(-delta, e[i], t[i]) * a.scale;
     const int64_t bh = row / a.N, n = row % a.N;
+    const float scale = keys_of(a, a.Bk == a.B ? (int)(bh / a.H) : 0) == 1 ? 0.f : a.scale;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = fmaf(-delta, e[i], t[i]) * scale;
     store8(static_cast<T *>(a.dq) + (bh / a.H) * a.dqB + (bh % a.H) * a.dqH + n * a.dqN + c8 * 8, t);
     if (c8 == 0) a.ndelta[padded_row(a, (int)(bh / a.H), (int)(bh % a.H), (int)n)] -= delta;
 }
@@ -823,6 +827,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (ok && wait.warp(&bar.acc_full, 0, 0x6a)) {
             tc_fence_after();
             const int key_at = kt * kT + key;
+            const float scale = nk == 1 ? 0.f : a.scale;
             const int64_t at = ((int64_t)split * a.sets + set) * a.M + key_at;
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
@@ -841,7 +846,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 tmem_wait_ld();
                 if (key_at < nk) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]) * a.scale;
+                    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]) * scale;
 #pragma unroll
                     for (int i = 0; i < 32; i += 8) store8(a.part_dk + at * D + col + i, f + i);
                 }

@@ -215,19 +215,20 @@ __global__ void __launch_bounds__(kFewThreads) cross_few_kernel(const __grid_con
     cluster.sync();  // nobody leaves while its sums are read
 }
 
-// p and dp of the CTA's keys; sums of each warp and of the CTA: p dp k, p k, p dp.
+// p and dp of the CTA's keys; sums of each warp and of the CTA: p dp k, p k, p dp
+// and the keys that are read.
 template <int D, int R>
 constexpr size_t few_bwd_smem(int keys)
 {
-    return ((size_t)keys * R * 2 + (size_t)(kFewWarps + 1) * R * (2 * D + 1) + R) * 4;
+    return ((size_t)keys * R * 2 + (size_t)(kFewWarps + 1) * R * (2 * D + 2) + R) * 4;
 }
 
 template <typename T, int D, int R>
-__global__ void __launch_bounds__(kFewThreads) cross_few_bwd_kernel(const __grid_constant__ CrossArgs a, int cap)
+__global__ void __launch_bounds__(kFewThreads, R == 1 ? 3 : R == 2 ? 2 : 1) cross_few_bwd_kernel(const __grid_constant__ CrossArgs a, int cap)
 {
     // with one row the registers of rows under way cost more (CTAs a SM) than they give: 30 us for 35
     constexpr bool kAhead = R > 1;
-    constexpr int LPR = D / 8, NG = kFewThreads / LPR, U = 2, S = 2 * D + 1;
+    constexpr int LPR = D / 8, NG = kFewThreads / LPR, U = 2, S = 2 * D + 2;
     extern __shared__ __align__(16) float few_smem[];
     float2 *pd = reinterpret_cast<float2 *>(few_smem);        // [cap][R]
     float *w_s = few_smem + (size_t)cap * R * 2;              // [warps][R][S]
@@ -240,7 +241,7 @@ __global__ void __launch_bounds__(kFewThreads) cross_few_bwd_kernel(const __grid
     const T *k = static_cast<const T *>(a.k) + w.bk * a.kB + w.hk * a.kH + c8 * 8;
     const T *v = static_cast<const T *>(a.v) + w.bk * a.vB + w.hk * a.vH + c8 * 8;
     const uint8_t *mask = a.mask ? a.mask + w.bk * a.mask_stride : nullptr;
-    float q[R][8], y[R][8], t[R][8], e[R][8], nl[R], delta[R];
+    float q[R][8], y[R][8], t[R][8], e[R][8], nl[R], delta[R], count = 0.f;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const FewRow x = few_row(a, w.bk, w.hk, min(r, rows - 1));
@@ -276,6 +277,7 @@ __global__ void __launch_bounds__(kFewThreads) cross_few_bwd_kernel(const __grid
         for (int u = 0; u < U; ++u) {
             const int key = k0 + u * NG + g;
             const bool on = next[u];
+            if (on) count += 1.f;
             float x[8], z[8];
             kr[u].values(x);
             vr[u].values(z);
@@ -306,6 +308,8 @@ __global__ void __launch_bounds__(kFewThreads) cross_few_bwd_kernel(const __grid
         }
     }
 #pragma unroll
+    for (int x = LPR; x < 32; x <<= 1) count += __shfl_xor_sync(0xffffffffu, count, x);
+#pragma unroll
     for (int r = 0; r < R; ++r) {
 #pragma unroll
         for (int x = LPR; x < 32; x <<= 1) {
@@ -323,7 +327,10 @@ __global__ void __launch_bounds__(kFewThreads) cross_few_bwd_kernel(const __grid
                 dst[c8 * 8 + i] = t[r][i];
                 dst[D + c8 * 8 + i] = e[r][i];
             }
-            if (c8 == 0) dst[2 * D] = delta[r];
+            if (c8 == 0) {
+                dst[2 * D] = delta[r];
+                dst[2 * D + 1] = count;
+            }
         }
     }
     __syncthreads();
@@ -333,6 +340,10 @@ __global__ void __launch_bounds__(kFewThreads) cross_few_bwd_kernel(const __grid
         c_s[x] = s;
     }
     cluster.sync();
+    // of a single key p is 1 whatever its score: no gradient reaches q and k, not even the roundings of dp - D
+    float keys = 0.f;
+    for (int x = 0; x < ranks; ++x) keys += cluster.map_shared_rank(c_s, x)[2 * D + 1];
+    const float scale = keys == 1.f ? 0.f : a.scale;
     if (threadIdx.x < R) {
         float s = 0.f;
         for (int x = 0; x < ranks; ++x) s += cluster.map_shared_rank(c_s, x)[threadIdx.x * S + 2 * D];
@@ -350,7 +361,7 @@ __global__ void __launch_bounds__(kFewThreads) cross_few_bwd_kernel(const __grid
             }
             const FewRow z = few_row(a, w.bk, w.hk, r);
             T *dst = static_cast<T *>(a.dq) + z.b * a.dqB + z.h * a.dqH + z.n * a.dqN + d;
-            *reinterpret_cast<uint16_t *>(dst) = (uint16_t)pack2(T(), fmaf(-s_D[r], se, st) * a.scale, 0.f);
+            *reinterpret_cast<uint16_t *>(dst) = (uint16_t)pack2(T(), fmaf(-s_D[r], se, st) * scale, 0.f);
         }
     // dk, dv of the range, zeros where no row reads the key
     T *dk = static_cast<T *>(a.dk) + w.bk * a.dkB + w.hk * a.dkH + c8 * 8;
@@ -364,7 +375,7 @@ __global__ void __launch_bounds__(kFewThreads) cross_few_bwd_kernel(const __grid
         for (int r = 0; r < R; ++r) {
             const float2 x = pd[(key - w.k0) * R + r];
             if (x.x == 0.f) continue;  // (NaN is not)
-            const float ds = x.x * (x.y - D_r[r]) * a.scale;
+            const float ds = x.x * (x.y - D_r[r]) * scale;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 sk[i] = fmaf(ds, q[r][i], sk[i]);

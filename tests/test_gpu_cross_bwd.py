@@ -168,3 +168,26 @@ def test_refusals_on_the_device():
         scope.cross_attn_backward(q, q, k, k, o, lse.double())
     with pytest.raises(scope.ScopeError, match="overlap"):
         scope.cross_attn_backward(q, q, k, k, o, lse, dq=q)
+
+
+@pytest.mark.parametrize("N", [1, 3, 40, 300])
+@pytest.mark.parametrize("M,mask", [(1, "all"), (300, "len"), (300, "mask"), (5000, "len")])
+def test_a_single_key_has_no_gradient_through_its_score(N, M, mask):
+    """p is 1 whatever the score: dq and dk are zero, not what roundings leave; dv is the sum of do,
+    rounded once after a sum in 32 bits of p and do within 2^-18 + 2^-8 of themselves (p next to 1
+    may round to its 16-bit neighbour)."""
+    q, do = rand((2, 2, N, 64), BF16, 1), rand((2, 2, N, 64), BF16, 4)
+    k, v = rand((2, 2, M, 64), BF16, 2), rand((2, 2, M, 64), BF16, 3)
+    kw = {}
+    if mask == "len":
+        kw = dict(kv_len=torch.ones(2, dtype=torch.int32, device=DEV))
+    elif mask == "mask":
+        kw = dict(kv_mask=torch.zeros((2, M), dtype=torch.bool, device=DEV))
+        kw["kv_mask"][:, 123] = True
+    got = grads(q, k, v, do, **kw)
+    scope.ops_sync_status()
+    at = 123 if mask == "mask" else 0
+    assert (got["dq"] == 0).all() and (got["dk"] == 0).all()
+    want, size = do.double().sum(2), do.double().abs().sum(2)
+    assert ((got["dv"][:, :, at].double() - want).abs() <= size * (2.0 ** -18 + 2.0 ** -8) + want.abs() * 2.0 ** -8).all()
+    assert torch.equal(got["o"], v[:, :, at:at + 1].expand_as(q))
