@@ -325,6 +325,8 @@ scope_status scope_kmeans_noalloc(const scope_tensor *x, int32_t dim_off, int32_
 /*     dy (the very same rows).                                             */
 /*   - equal calls give equal bits: no sum depends on the order of atomics. */
 /*   - a bounded wait that runs out is reported by scope_ops_sync_status.   */
+/*   - a workspace serves one call at a time: calls, or captured graphs,    */
+/*     that may run at once need one each.                                  */
 /* ---------------------------------------------------------------------- */
 
 /* Positions of the tokens on the (t, h, w) axes: int32 [B][N][3], device,
@@ -393,7 +395,8 @@ typedef struct {
  *          (masked: whether a mask is given).
  * B*H*N <= 2^30.  Scores, softmax statistics and sums are held in 32 bits;
  * softmax weights (and in the backward pass ds) are rounded to the inputs' type as
- * operands of the tensor cores. */
+ * operands of the tensor cores (not where at most four rows read a key head,
+ * which the tensor cores do not serve). */
 size_t scope_cross_attn_workspace_bytes(const scope_tensor *q, const scope_tensor *k, int masked);
 scope_status scope_cross_attn(const scope_tensor *q, const scope_tensor *k, const scope_tensor *v,
                               const scope_keys *keys, float scale, scope_tensor *o, float *lse, void *workspace,
@@ -404,7 +407,8 @@ scope_status scope_cross_attn(const scope_tensor *q, const scope_tensor *k, cons
  *   d_o, dq    [B,H,N,D], q's dtype.
  *   dk, dv     [Bk,Hk,M,D], q's dtype, written in full: summed over the query
  *              heads of a key head and, for Bk = 1, over the batch; zero for keys
- *              that no row may read.
+ *              that no row may read.  Where a row reads a single key, its score
+ *              has no gradient: exactly zero.
  *   workspace  >= scope_cross_attn_backward_workspace_bytes bytes, 256-B aligned.
  * With f16, ds = p (dp - d_o . o) is held in f16: scale the loss as usual. */
 size_t scope_cross_attn_backward_workspace_bytes(const scope_tensor *q, const scope_tensor *k, int masked);
