@@ -659,27 +659,30 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         bar.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    // keys of a list, or a last tile that ends inside its set, are copied by all threads
+    const bool whole = tma_keys<kT>(a, nk, kt);
+    if (!whole) {
+        const int32_t *list = a.idx ? a.idx + (int64_t)bk * a.M : nullptr;
+        copy_keys<T, D, kT, kBwdThreads>(list, nk, kt, static_cast<const T *>(a.k) + bk * a.kB + hk * a.kH, a.kN, sK);
+        copy_keys<T, D, kT, kBwdThreads>(list, nk, kt, static_cast<const T *>(a.v) + bk * a.vB + hk * a.vH, a.vN, sV);
+        cp_async_commit();
+        cp_async_wait_all();
+        fence_async_smem();
+    }
     bwd_prologue(warp, &bar.tmem_base);
     const uint32_t tmem = uniform(bar.tmem_base);
     const Waiter wait{&bar.abort, g_cross_bwd_err};
 
     if (warp == 8) {
         // ------------------------------------------------------------ K, V
-        if (tma_keys<kT>(a, nk, kt)) {
-            if (lane == 0) {
+        if (lane == 0) {
+            if (whole) {
                 mbar_expect_tx(&bar.kv_full, 2 * TB);
                 tma_tile<D>(sK, &m.k, kt * kT, hk, bk, &bar.kv_full);
                 tma_tile<D>(sV, &m.v, kt * kT, hk, bk, &bar.kv_full);
+            } else {
+                mbar_arrive(&bar.kv_full);
             }
-        } else {
-            const int32_t *list = a.idx ? a.idx + (int64_t)bk * a.M : nullptr;
-            copy_keys<T, D, kT>(list, nk, kt, static_cast<const T *>(a.k) + bk * a.kB + hk * a.kH, a.kN, sK);
-            copy_keys<T, D, kT>(list, nk, kt, static_cast<const T *>(a.v) + bk * a.vB + hk * a.vH, a.vN, sV);
-            cp_async_commit();
-            cp_async_wait_all();
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.kv_full);
         }
     } else if (warp == 9 || warp == 10) {
         // ------------------------------------------------------------ Q rows, dO rows

@@ -426,15 +426,15 @@ __device__ __forceinline__ void store_row(float *p, const uint32_t *x)
     for (int i = 0; i < N; i += 8) store32(p + i, x + i);
 }
 
-// One warp copies the keys of tile j (rows of a key list, if any) into a tile,
+// THREADS threads (one warp, or a block) copy the keys of tile j (rows of a key list, if any) into a tile,
 // rows past the set's nk keys as zeros: their memory is never read.
-template <typename T, int D, int ROWS>
+template <typename T, int D, int ROWS, int THREADS = 32>
 __device__ __noinline__ void copy_keys(const int32_t *list, int nk, int j, const T *base, int64_t sn, uint32_t dst)
 {
-    constexpr int CH = D / 8, RPI = 32 / CH;
-    const int lane = threadIdx.x & 31, ch = lane % CH;
+    constexpr int CH = D / 8, RPI = THREADS / CH;
+    const int tid = THREADS == 32 ? threadIdx.x & 31 : threadIdx.x, ch = tid % CH;
 #pragma unroll 8
-    for (int i = lane / CH; i < ROWS; i += RPI) {
+    for (int i = tid / CH; i < ROWS; i += RPI) {
         const int kj = j * ROWS + i;
         const bool ok = kj < nk;
         const int key = ok ? (list ? list[kj] : kj) : 0;
