@@ -117,16 +117,27 @@ def _stream(stream, device=None) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _strides(x: torch.Tensor, name: str) -> tuple:
+    """x's strides for the library, where all zeros mean the contiguous layout: a
+    single element that was expanded (as the gradient of a sum is) would be read
+    as a tensor of its shape, far past its memory."""
+    s = x.stride()
+    if not any(s) and x.numel():
+        raise ValueError(f"{name}: one element expanded to {list(x.shape)}; contiguous() makes a tensor of it")
+    return s
+
+
 def as_tensor(x: torch.Tensor) -> ScopeTensor:
     """scope_tensor of a [B, H, N, D] tensor with its element strides (the
     library checks them: last stride 1, 16-byte aligned rows, no overlap)."""
     if x.dim() != 4:
         raise ValueError("expected a [B, H, N, D] tensor")
+    strides = _strides(x, "tensor")
     dt = {torch.float32: SCOPE_F32, torch.bfloat16: SCOPE_BF16}.get(x.dtype)
     if dt is None:
         raise ValueError(f"unsupported dtype {x.dtype}")
     B, H, N, D = x.shape
-    return ScopeTensor(x.data_ptr(), dt, B, H, N, D, (ctypes.c_int64 * 4)(*x.stride()))
+    return ScopeTensor(x.data_ptr(), dt, B, H, N, D, (ctypes.c_int64 * 4)(*strides))
 
 
 def make_params(w=None, **kw):

@@ -18,7 +18,7 @@ from typing import Optional
 
 import torch
 
-from . import ScopeGrid, ScopeParams, ScopeTensor, ScopeError, _check, lib
+from . import ScopeGrid, ScopeParams, ScopeTensor, ScopeError, _check, _strides, lib
 
 SCOPE_F16 = 4
 _DT = {torch.float32: 0, torch.bfloat16: 1, torch.float16: SCOPE_F16}
@@ -79,7 +79,7 @@ def _tensor(x: torch.Tensor, name: str) -> bytes:
     dt = _DT.get(x.dtype)
     if dt is None:
         raise ValueError(f"{name}: unsupported dtype {x.dtype}")
-    return _TENSOR(x.data_ptr(), dt, *x.shape, *x.stride())
+    return _TENSOR(x.data_ptr(), dt, *x.shape, *_strides(x, name))
 
 
 def _vector(x: torch.Tensor, D: int, name: str) -> bytes:
