@@ -140,6 +140,14 @@ def as_tensor(x: torch.Tensor) -> ScopeTensor:
     return ScopeTensor(x.data_ptr(), dt, B, H, N, D, (ctypes.c_int64 * 4)(*strides))
 
 
+def _whole(workspace: torch.Tensor) -> torch.Tensor:
+    """A given workspace, whose bytes the library writes in a row: of a view with gaps or
+    repeats they would be others' bytes, or past its memory."""
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace
+
+
 def make_params(w=None, **kw):
     """(ScopeParams, ScopeGrid) from a synth.Workload and/or keyword overrides."""
     f = {}
@@ -204,7 +212,7 @@ def plan(q: torch.Tensor, k: torch.Tensor, params: ScopeParams, grid: ScopeGrid,
     """Steps 1-4 on the device: returns a Plan whose results stay in `workspace`."""
     tq, tk = as_tensor(q), as_tensor(k)
     need = workspace_bytes(q, params, grid)
-    if workspace is None or workspace.numel() < need:
+    if workspace is None or _whole(workspace).numel() < need:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     h = ctypes.c_void_p()
     with torch.cuda.device(q.device):
@@ -233,7 +241,7 @@ def dense_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, params: ScopeP
     need = lib().scope_dense_workspace_bytes(ctypes.byref(tq), ctypes.byref(grid), ctypes.byref(params))
     if need == 0:
         raise ScopeError(1, lib().scope_last_error().decode())
-    if workspace is None or workspace.numel() < need:
+    if workspace is None or _whole(workspace).numel() < need:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     if out is None:
         out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)

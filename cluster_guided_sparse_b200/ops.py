@@ -18,7 +18,7 @@ from typing import Optional
 
 import torch
 
-from . import ScopeGrid, ScopeParams, ScopeTensor, ScopeError, _check, _strides, lib
+from . import ScopeGrid, ScopeParams, ScopeTensor, ScopeError, _check, _strides, _whole, lib
 
 SCOPE_F16 = 4
 _DT = {torch.float32: 0, torch.bfloat16: 1, torch.float16: SCOPE_F16}
@@ -135,7 +135,7 @@ class _Launch:
             return x.new_empty(shape, dtype=dtype)
 
     def workspace(self, x: torch.Tensor, given: Optional[torch.Tensor], need: int) -> torch.Tensor:
-        if given is not None and given.numel() * given.element_size() >= need:
+        if given is not None and _whole(given).numel() * given.element_size() >= need:
             return given
         return self.empty(x, (need,), torch.uint8)
 
