@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
-            mbar_init(&q_empty[i], 8);
+            mbar_init(&q_empty[i], 8);  // the softmax warps, or for those without rows their issuer
             for (int b = 0; b < 2; ++b) {
                 mbar_init(&s_full[i][b], 1);
                 mbar_init(&p_full[i][b], 4);
@@ -228,7 +228,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_
             mid = 0;
             if (more) {  // S = Q K^T
                 const int buf = front.seq & 1;
-                if (!(ok = wait.all(&k_full[kr.slot], kr.use & 1, 0x44, &q_full[buf], (front.seq >> 1) & 1, 0x43))) break;
+                // Q once an item, and by both issuers: nothing frees the item's buffer before this one has looked at
+                // it, so its barrier is never two phases ahead, nor one behind of an item that was passed over
+                ok = front.first ? wait.all(&k_full[kr.slot], kr.use & 1, 0x44, &q_full[buf], (front.seq >> 1) & 1, 0x43)
+                                 : wait.warp(&k_full[kr.slot], kr.use & 1, 0x44);
+                if (!ok) break;
                 mid = kStep | (front.first ? kFirst : 0) | (front.j + 1 == front.t1 ? kLast : 0);
                 if (t < front.nt) {
                     mid |= kHas;
@@ -246,6 +250,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_
                     __syncwarp();
                     ++ns;
                 } else if (lane == 0) {
+                    if (front.first) mbar_arrive(&q_empty[buf], 4);  // for the row tile's softmax warps, which have no rows
                     mbar_arrive(&k_empty[kr.slot]);
                 }
                 kr.next();
@@ -271,11 +276,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_
         for (int item = blockIdx.x; ok && item < a.items; item += gridDim.x) {
             const bool some = w.t0 < w.t1;  // uniform for the CTA
             const int buf = qi & 1;
-            if (w.r.nq <= t * kTile) {  // no rows here: the item's Q is free, once it has come
+            if (w.r.nq <= t * kTile) {  // no rows here: the row tile's issuer frees the item's Q
                 if (some) {
                     if (leaving) q_free();
-                    if (!(ok = wait.warp(&q_full[buf], (qi >> 1) & 1, 0x4c))) break;
-                    if (lane == 0) mbar_arrive(&q_empty[buf]);
                     ++qi;
                 }
                 w = fwd_item(a, item + gridDim.x);
