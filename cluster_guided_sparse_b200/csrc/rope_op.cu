@@ -265,15 +265,20 @@ __global__ void __launch_bounds__(kRopeThreads, 2)
                 }
                 const float r = rsqrtf(row_sum<LPR>(dot(xr, xr)) * (1.f / D) + a.eps);
                 const float m = -row_sum<LPR>(dot(g, xr)) * (1.f / D) * r * r;
-                const float rs = store ? r : 0.f;
-                const F2 r2(r, r), mm(m, m), rs2(rs, rs);
+                const F2 r2(r, r), mm(m, m);
+                // Rows that are not this thread's are left out, not multiplied by zero: an idle lane may hold an
+                // infinity, in place even one that the row's own lanes have just written.
+                if (store) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        dwr.e[i] = fma2(dz.e[i], xr.e[i] * r2, dwr.e[i]);
+                        dwr.o[i] = fma2(dz.o[i], xr.o[i] * r2, dwr.o[i]);
+                    }
+                }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     g.e[i] = fma2(xr.e[i], mm, g.e[i]) * r2;
                     g.o[i] = fma2(xr.o[i], mm, g.o[i]) * r2;
-                    // (rows that are not this thread's count nothing)
-                    dwr.e[i] = fma2(dz.e[i], xr.e[i] * rs2, dwr.e[i]);
-                    dwr.o[i] = fma2(dz.o[i], xr.o[i] * rs2, dwr.o[i]);
                 }
                 float o[8];
                 g.get(o);
