@@ -40,6 +40,10 @@
 //
 // p and ds are rounded to the inputs' 16-bit type as operands of the products
 // (the tensor cores take 16-bit operands); S, dP, D, lse and all sums are fp32.
+// f16's smallest normal number is 2^-14, which the p of a flat row passes at 16000
+// keys (at 60000 its rounding was 4 times that of a normal number, and from 2^25 on
+// p vanished), so f16 holds p 2^14; the power is added to -lse and taken off dP and
+// D' (whose sum and product with p then give ds as it is), dv and E.
 // Barriers, rings, bounded waits as in cross_attn.cu.
 #include "cross_common.cuh"
 
@@ -63,6 +67,22 @@ constexpr size_t bwd_smem(int D) { return (size_t)kTiles * kT * D * 2 + kFloats 
 // Column of 16-element step k of p (ds: 32 further on) as an A operand: the 64
 // values of each half of the warps sit, packed, in the half's own columns of S.
 __device__ __forceinline__ uint32_t half_col(int k) { return (uint32_t)((k >> 2) * 64 + (k & 3) * 8); }
+
+// Softmax weights are held as p 2^kUp: p is 1 at most, up to the error of lse, so a
+// factor of 4 is left in f16.  kDown = 2^-kUp.
+template <typename T> constexpr float kUp = 0.f;
+template <> constexpr float kUp<__half> = 14.f;
+template <typename T> constexpr float kDown = 1.f;
+template <> constexpr float kDown<__half> = 1.f / 16384.f;
+
+// dP - D' of two values, by 2^-kUp (nd is).
+template <typename T>
+__device__ __forceinline__ uint64_t dp_less_d(uint32_t dp0, uint32_t dp1, uint64_t nd)
+{
+    const uint64_t dp = f2pack(__uint_as_float(dp0), __uint_as_float(dp1));
+    if constexpr (kUp<T> == 0.f) return fadd2(dp, nd);
+    else return ffma2(dp, f2pack(kDown<T>, kDown<T>), nd);
+}
 
 // rows x cols = A B^T of two [128][D] tiles.
 template <typename T, int D>
@@ -144,9 +164,9 @@ __device__ __forceinline__ DqItem dq_item(const CrossArgs &a, int item)
     return w;
 }
 
-// -D' (do . o, of the rounded o) of 16 rows of a tile by each of eight warps, and
-// -lse in base 2 of this thread's own row: -inf, so that p is 0, where the row
-// reads nothing or does not exist.
+// -D' (do . o, of the rounded o) 2^-kUp of 16 rows of a tile by each of eight warps,
+// and kUp - lse in base 2 of this thread's own row: -inf, so that p is 0, where the
+// row reads nothing or does not exist.
 template <typename T, int D>
 __device__ __forceinline__ float row_values(const CrossArgs &a, RowTile w, int hk, float *s_nd)
 {
@@ -174,7 +194,7 @@ __device__ __forceinline__ float row_values(const CrossArgs &a, RowTile w, int h
     if (row < w.nq) {
         tile_row(a, w, hk, row, b, h, n);
         const float lse = a.lse[((int64_t)b * a.H + h) * a.N + n];
-        if (lse != -INFINITY) nl = -lse * 1.4426950408889634f;
+        if (lse != -INFINITY) nl = fmaf(-lse, 1.4426950408889634f, kUp<T>);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -185,7 +205,7 @@ __device__ __forceinline__ float row_values(const CrossArgs &a, RowTile w, int h
         for (int e = 0; e < 8; ++e) sum = fmaf(x[e], z[e], sum);
 #pragma unroll
         for (int e = LPR >> 1; e > 0; e >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, e);
-        if (c8 == 0) s_nd[warp * 16 + u * RPP + lane / LPR] = -sum;
+        if (c8 == 0) s_nd[warp * 16 + u * RPP + lane / LPR] = -sum * kDown<T>;
     }
     return nl;
 }
@@ -452,7 +472,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     const uint64_t t2 = fmul2(f2pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])),
-                                              fadd2(f2pack(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1])), ndp));
+                                              dp_less_d<T>(d[2 * i], d[2 * i + 1], ndp));
                     if (i & 1) dB = fadd2(dB, t2);
                     else dA = fadd2(dA, t2);
                     float x0, x1;
@@ -492,7 +512,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     if (a.dq_splits > 1 && store) a.part_delta[part] = delta;
                     if (w.split == 0 || a.dq_splits == 1) {
                         a.nlse[w.at + row] = nl;
-                        a.ndelta[w.at + row] = a.dq_splits > 1 ? nd : nd - delta;
+                        a.ndelta[w.at + row] = a.dq_splits > 1 ? nd : fmaf(-delta, kDown<T>, nd);
                     }
                 }
             } else if (store) {
@@ -549,7 +569,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     float f[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        f[i] = fmaf(-delta, __uint_as_float(e[i]), __uint_as_float(r[i])) * scale;
+                        f[i] = fmaf(-delta * kDown<T>, __uint_as_float(e[i]), __uint_as_float(r[i])) * scale;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) u[c * 4 + i] = pack8<T>(f + 8 * i);
                     // a half row is one box's 64 columns at D = 128
@@ -598,9 +618,9 @@ __global__ void __launch_bounds__(256) cross_dq_join_kernel(const __grid_constan
     const int64_t bh = row / a.N, n = row % a.N;
     const float scale = keys_of(a, a.Bk == a.B ? (int)(bh / a.H) : 0) == 1 ? 0.f : a.scale;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = fmaf(-delta, e[i], t[i]) * scale;
+    for (int i = 0; i < 8; ++i) t[i] = fmaf(-delta * kDown<T>, e[i], t[i]) * scale;
     store8(static_cast<T *>(a.dq) + (bh / a.H) * a.dqB + (bh % a.H) * a.dqH + n * a.dqN + c8 * 8, t);
-    if (c8 == 0) a.ndelta[padded_row(a, (int)(bh / a.H), (int)(bh % a.H), (int)n)] -= delta;
+    if (c8 == 0) a.ndelta[padded_row(a, (int)(bh / a.H), (int)(bh % a.H), (int)n)] -= delta * kDown<T>;
 }
 
 // ---------------------------------------------------------------- dk, dv
@@ -811,12 +831,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 const ulonglong2 n2 = nd[c];
                 float x0, x1;
                 f2unpack(fmul2(f2pack(__uint_as_float(r[4 * c]), __uint_as_float(r[4 * c + 1])),
-                               fadd2(f2pack(__uint_as_float(d[4 * c]), __uint_as_float(d[4 * c + 1])), n2.x)),
+                               dp_less_d<T>(d[4 * c], d[4 * c + 1], n2.x)),
                          x0, x1);
                 d[4 * c] = __float_as_uint(x0);
                 d[4 * c + 1] = __float_as_uint(x1);
                 f2unpack(fmul2(f2pack(__uint_as_float(r[4 * c + 2]), __uint_as_float(r[4 * c + 3])),
-                               fadd2(f2pack(__uint_as_float(d[4 * c + 2]), __uint_as_float(d[4 * c + 3])), n2.y)),
+                               dp_less_d<T>(d[4 * c + 2], d[4 * c + 3], n2.y)),
                          x0, x1);
                 d[4 * c + 2] = __float_as_uint(x0);
                 d[4 * c + 3] = __float_as_uint(x1);
@@ -841,7 +861,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 tmem_wait_ld();
                 if (key_at < nk) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]);
+                    for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]) * kDown<T>;
 #pragma unroll
                     for (int i = 0; i < 32; i += 8) store8(a.part_dv + at * D + col + i, f + i);
                 }

@@ -79,7 +79,7 @@ struct CrossArgs {
     int64_t dB, dH, dN;
     int tiles;                 // 128-row tiles per set
     // per set, tile and row: -lse in base 2 (-inf where the row reads nothing or
-    // does not exist: its p is then 0) and -D
+    // does not exist: its p is then 0) and -D (f16: with p's power of two, and less it)
     float *nlse, *ndelta;
     void *dq;
     int64_t dqB, dqH, dqN;

@@ -410,7 +410,8 @@ scope_status scope_cross_attn(const scope_tensor *q, const scope_tensor *k, cons
  *              that no row may read.  Where a row reads a single key, its score
  *              has no gradient: exactly zero.
  *   workspace  >= scope_cross_attn_backward_workspace_bytes bytes, 256-B aligned.
- * With f16, ds = p (dp - d_o . o) is held in f16: scale the loss as usual. */
+ * With f16, ds = p (dp - d_o . o) is held in f16: scale the loss as usual (p needs
+ * no scaling: it is held with a power of two that keeps 2^-28 a normal number). */
 size_t scope_cross_attn_backward_workspace_bytes(const scope_tensor *q, const scope_tensor *k, int masked);
 scope_status scope_cross_attn_backward(const scope_tensor *d_o, const scope_tensor *q, const scope_tensor *k,
                                        const scope_tensor *v, const scope_tensor *o, const float *lse,
