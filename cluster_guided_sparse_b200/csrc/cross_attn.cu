@@ -32,7 +32,10 @@
 // rescale: O and l move to a new maximum only when it grew by more than 2^8,
 // so P stays below 2^8.  P is rounded to the inputs' type for the product
 // (the tensor cores take 16-bit operands); its sum l is taken before that
-// rounding, in fp32, as are S, O and lse.
+// rounding, in fp32, as are S, O and lse.  f16 holds P 2^7 (up to 2^15), of which l and O
+// are made alike, so that weights down to 2^-21 of the largest are normal numbers: of a
+// long tail of small ones, as a whole no small share of o, each is else off by more than
+// a rounding (3% at 2^-20).
 //
 // Few rows (a single token, a short prompt reading a long video) leave most
 // SMs without an item: the keys are then split into ranges whose normalised
@@ -59,6 +62,10 @@ constexpr int kTile = 128;  // rows of a Q tile
 
 constexpr int fwd_stages(int D) { return D == 128 ? 3 : 6; }  // of K and of V
 constexpr size_t fwd_smem(int D) { return (size_t)(4 * kTile + 2 * fwd_stages(D) * kFwdKeys) * D * 2 + 1024; }
+
+// P and its sums are held by 2^kFwdUp.
+template <typename T> constexpr float kFwdUp = 0.f;
+template <> constexpr float kFwdUp<__half> = 7.f;
 
 struct FwdItem {
     int bk, hk, t0, t1, nk, split;
@@ -332,7 +339,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_
                     }
                 }
                 const float m_ref = m_run == -INFINITY ? 0.f : m_run;
-                const uint64_t nmp = f2pack(-m_ref, -m_ref);
+                const uint64_t nmp = f2pack(kFwdUp<T> - m_ref, kFwdUp<T> - m_ref);
 #pragma unroll
                 for (int c = 0; c < kFwdKeys / 32; ++c) {
                     uint32_t pk[16];
@@ -369,7 +376,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_
             T *o = static_cast<T *>(a.o) + b * a.oB + h * a.oH + n * a.oN;
             float *po = a.part_o + part * D;
             if (store) {
-                const float lse2 = l == 0.f ? -INFINITY : m_run + log2f(l);
+                const float lse2 = l == 0.f ? -INFINITY : m_run + (log2f(l) - kFwdUp<T>);
                 if (a.splits > 1) a.part_lse[part] = lse2;
                 else if (a.lse) a.lse[flat] = lse2 * 0.6931471805599453f;
             }

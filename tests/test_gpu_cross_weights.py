@@ -85,3 +85,28 @@ def test_values_and_keys_with_a_common_offset(dtype, N, M, D):
         for n in caught:  # a kernel that kept do . o of the rounded o would be seen
             caught[n] |= bool(((wrong[n] - val[n]).abs() > b[n]).any())
     assert caught["dq"] and (caught["dk"] or N > 8), caught
+
+
+@pytest.mark.parametrize("N", [5, 200])
+@pytest.mark.parametrize("M", [200, 4096])
+def test_a_tail_of_small_weights_behind_a_large_one(M, N):
+    """Forward: one key of weight 1 and value 0, the others of weight P = 16.5 2^-24 and value 1 (16.5 of
+    f16's subnormal steps): o = T / (1 + T), T the tail's sum.  P is known to 2^-18 (its exponent's scale is
+    rounded, 2^-23 of 20 and less, and the exponential 2^-22), its 16 bits add h = 2^-11, the sums acc.  The
+    row's sum is four fp32 sums of a quarter of the weights each; the one with the large weight rounds each
+    addition to 2^-24 of itself, at most, so lse is off by M / 4 of those and 2^-21 of itself."""
+    H, D = 150, 64  # more items than CTAs: the keys are not split
+    q, k = (torch.zeros((1, H, n, D), dtype=F16, device=DEV) for n in (N, M))
+    q[..., 0], k[..., 0, 0] = 1.0, 1.0
+    v = torch.ones((1, H, M, D), dtype=F16, device=DEV)
+    v[:, :, 0] = 0.0
+    P = 16.5 * 2.0 ** -24
+    scale = -float(torch.log(torch.tensor(P, dtype=torch.float64)))
+    o, lse = scope.cross_attn(q, k, v, scale=scale, return_lse=True)
+    scope.ops_sync_status()
+    T = (M - 1) * P
+    want = torch.full_like(o, T / (1 + T), dtype=torch.float64)
+    acc = (M / 16 + 16) * 2.0 ** -23
+    R.within(o, want, want * (2.0 ** -11 + 2.0 ** -17 + 2 * acc) + R.half_ulp(want, F16), "o")
+    want = torch.full_like(lse, scale, dtype=torch.float64) + torch.log1p(torch.tensor(T, dtype=torch.float64))
+    R.within(lse, want, 2.0 ** -21 * want + M / 4 * 2.0 ** -24, "lse")
