@@ -283,4 +283,5 @@ def kmeans_noalloc(x: torch.Tensor, dim_off: int, dim_n: int, C: int, iters: int
     return labels, centroids
 
 
-from .ops import cross_attn, cross_attn_backward, ops_sync_status, rope, rope_backward  # noqa: E402  (the operators build on the names above)
+from .ops import (cross_attn, cross_attn_backward, ops_selftest_wait_timeout, ops_sync_status, rope,  # noqa: E402
+                  rope_backward)  # (the operators build on the names above)

@@ -523,6 +523,12 @@ cudaError_t cross_fwd_error(int32_t *err, bool clear)
     return e;
 }
 
+int32_t *cross_fwd_error_word()
+{
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, g_cross_err) == cudaSuccess ? static_cast<int32_t *>(p) : nullptr;
+}
+
 // Key ranges per row tile: the count with the least modelled time, in steps of
 // one 64-key tile (some 0.7 us a CTA).  An item costs its tiles and about four
 // more for its Q rows and epilogue; a split adds a launch (about 5 steps) and

@@ -937,6 +937,12 @@ cudaError_t cross_bwd_error(int32_t *err, bool clear)
     return e;
 }
 
+int32_t *cross_bwd_error_word()
+{
+    void *p = nullptr;
+    return cudaGetSymbolAddress(&p, g_cross_bwd_err) == cudaSuccess ? static_cast<int32_t *>(p) : nullptr;
+}
+
 // Ranges of `len` tiles for `items` pieces of work: the count with the least
 // modelled time in tile steps (some 1.3 us), a piece costing its tiles and
 // `fixed` more, a range's partial sums `part` steps of join traffic.

@@ -486,6 +486,8 @@ void launch_cross_bwd(const CrossArgs &a, const CrossMaps &m, int D, bool f16, i
                       cudaStream_t st);
 cudaError_t cross_fwd_error(int32_t *err, bool clear);
 cudaError_t cross_bwd_error(int32_t *err, bool clear);
+int32_t *cross_fwd_error_word();  // its device address, or null
+int32_t *cross_bwd_error_word();
 
 }  // namespace op
 }  // namespace scope

@@ -13,6 +13,7 @@
 scope_status scope_set_error(scope_status s, const char *msg);
 
 namespace scope {
+void launch_wait_timeout(int32_t *err, long long limit, cudaStream_t st);
 namespace op {
 bool check_tensor(const scope_tensor *t, const char *name, int64_t min_n, scope_status *st);
 RowStrides strides_of(const scope_tensor *t);
@@ -598,4 +599,17 @@ extern "C" scope_status scope_ops_sync_status(void *stream)
     if (err[0] & kErrTimeout) return fail(SCOPE_ETIMEOUT, "a bounded device wait gave up (detail 0x%x)", err[1]);
     if (err[0]) return fail(SCOPE_EDEVICE, "device range check fired (flags 0x%x, detail 0x%x)", err[0], err[1]);
     return SCOPE_OK;
+}
+
+extern "C" scope_status scope_ops_selftest_wait_timeout(int backward, int64_t wait_cycles, void *stream)
+{
+    if (backward != 0 && backward != 1) return fail(SCOPE_EINVAL, "backward must be 0 or 1");
+    if (wait_cycles < 1000 || wait_cycles > 4000000000ll)
+        return fail(SCOPE_EINVAL, "wait_cycles must be in [1e3, 4e9]");
+    const scope_status st = check_device();
+    if (st != SCOPE_OK) return st;
+    int32_t *err = backward ? op::cross_bwd_error_word() : op::cross_fwd_error_word();
+    if (!err) return fail(SCOPE_ECUDA, "no address of the error word");
+    launch_wait_timeout(err, (long long)wait_cycles, (cudaStream_t)stream);
+    return launch_status("scope_ops_selftest_wait_timeout");
 }

@@ -69,6 +69,7 @@ def _bind(L, T, S, W, K):
     L.scope_cross_attn_backward_workspace_bytes.restype = Z
     L.scope_cross_attn_backward.argtypes = [T, T, T, T, T, V, K, F, T, T, T, V, Z, V]
     L.scope_ops_sync_status.argtypes = [V]
+    L.scope_ops_selftest_wait_timeout.argtypes = [ctypes.c_int, ctypes.c_int64, V]
     L.scope_last_error.restype = ctypes.c_char_p
     return L
 
@@ -282,3 +283,14 @@ def ops_sync_status(stream=None, device=None):
         stream = torch.cuda.current_stream(device)
     with torch.cuda.device(stream.device):
         _check(_functions().scope_ops_sync_status(stream.cuda_stream))
+
+
+def ops_selftest_wait_timeout(cycles: int = 2_000_000, *, backward: bool = False, stream=None, device=None):
+    """Enqueues the failure-handling self-test of ops_sync_status: a bounded wait
+    on a barrier that nothing completes, recorded where the forward (or backward)
+    kernels record theirs, so the next ops_sync_status raises ScopeError
+    (SCOPE_ETIMEOUT)."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    with torch.cuda.device(stream.device):
+        _check(_functions().scope_ops_selftest_wait_timeout(int(backward), int(cycles), stream.cuda_stream))

@@ -424,6 +424,13 @@ scope_status scope_cross_attn_backward(const scope_tensor *d_o, const scope_tens
  * or SCOPE_ECUDA.  Not during a stream capture. */
 scope_status scope_ops_sync_status(void *stream);
 
+/* Failure-handling self-test of that report, as scope_selftest_wait_timeout: a
+ * bounded wait on a barrier that nothing completes gives up after `wait_cycles`
+ * (1e3 to 4e9) SM cycles, so the next scope_ops_sync_status returns SCOPE_ETIMEOUT.
+ *   backward  which of the two error words takes it: 0 that of the forward
+ *             kernels, 1 that of the backward ones. */
+scope_status scope_ops_selftest_wait_timeout(int backward, int64_t wait_cycles, void *stream);
+
 /* Number of kernels this library has launched in this process so far (all
  * devices, all threads); a diagnostic for launch accounting. */
 int64_t scope_kernel_launches(void);
