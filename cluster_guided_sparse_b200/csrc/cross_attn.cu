@@ -235,11 +235,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_
             mid = 0;
             if (more) {  // S = Q K^T
                 const int buf = front.seq & 1;
-                // Q once an item, and by both issuers: nothing frees the item's buffer before this one has looked at
-                // it, so its barrier is never two phases ahead, nor one behind of an item that was passed over
-                ok = front.first ? wait.all(&k_full[kr.slot], kr.use & 1, 0x44, &q_full[buf], (front.seq >> 1) & 1, 0x43)
-                                 : wait.warp(&k_full[kr.slot], kr.use & 1, 0x44);
-                if (!ok) break;
+                // Q once an item (K again else), and by both issuers: nothing frees the item's buffer before this one has
+                // looked at it, so its barrier is never two phases ahead, nor one behind of an item that was passed over
+                uint64_t *k = &k_full[kr.slot], *q = front.first ? &q_full[buf] : k;
+                if (!(ok = wait.all(k, kr.use & 1, 0x44, q, (front.first ? front.seq >> 1 : kr.use) & 1, 0x43))) break;
                 mid = kStep | (front.first ? kFirst : 0) | (front.j + 1 == front.t1 ? kLast : 0);
                 if (t < front.nt) {
                     mid |= kHas;
@@ -338,8 +337,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) cross_fwd_kernel(const __grid_
                         tmem_st16(tO + c * 16, o);
                     }
                 }
-                const float m_ref = m_run == -INFINITY ? 0.f : m_run;
-                const uint64_t nmp = f2pack(kFwdUp<T> - m_ref, kFwdUp<T> - m_ref);
+                float shift = m_run == -INFINITY ? 0.f : -m_run;
+                if constexpr (kFwdUp<T> != 0.f) shift += kFwdUp<T>;
+                const uint64_t nmp = f2pack(shift, shift);
 #pragma unroll
                 for (int c = 0; c < kFwdKeys / 32; ++c) {
                     uint32_t pk[16];
