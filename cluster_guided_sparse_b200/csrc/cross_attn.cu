@@ -15,7 +15,8 @@
 // the L2 traffic.  The keys go in tiles of 64 with two S buffers a row tile, so
 // the products of the tile after next are out while the softmax works on this
 // one: neither waits for the other's latency (one buffer of 128 keys took 4200
-// clocks a row tile and 128 keys, of which the products are 1024).  The steps run on
+// clocks a row tile and 128 keys, of which the products are 1024; but then one warp
+// issued for both row tiles and was a limit too, see below).  The steps run on
 // over item borders: the next item's first S tiles are there before this one's
 // epilogue.  Q rows have two buffers for the same reason.
 //
@@ -41,9 +42,10 @@
 // SMs without an item: the keys are then split into ranges whose normalised
 // outputs and lse meet in cross_join_kernel, in a fixed order.
 //
-// Measured: 40 heads of 32760 rows x 512 keys 414 us (829 TFLOP/s; 17300 clocks an
+// Measured: 40 heads of 32760 rows x 512 keys 410 us (838 TFLOP/s; 17300 clocks an
 // item of 8 steps, 1700 a step, at the 1.5 to 1.7 GHz that the power cap leaves),
-// 24 heads of 118800 x 256 541 us, 24 heads of 77 x 118800 324 us (4.5 TB/s).
+// 24 heads of 118800 x 256 538 us, 24 heads of 77 x 118800 332 us (4.4 TB/s); on a card
+// that held its clock 353, 497 and 271.
 //
 // Every mbarrier wait is bounded (about two seconds); on timeout the thread
 // records it in the operators' error word, the CTA drops its items and all

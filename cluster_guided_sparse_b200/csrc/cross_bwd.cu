@@ -33,7 +33,7 @@
 // copies share.  Measured by clock: 2700 a step of the dk/dv kernel, 3400 of the
 // dq kernel, whose items add about 3500 each for their ends (a wait that is ready
 // takes some 60, so the issuers look at operands before they wait for the
-// softmax).  40 heads of 32760 rows x 512 keys: dq 790 us, dk/dv 560 us, the join 19.
+// softmax).  40 heads of 32760 rows x 512 keys: dq 774 us, dk/dv 573 us, the join 19.
 //
 // Rows split over CTAs (few keys, many rows) or keys split (few rows, many
 // keys) leave fp32 partial sums that a join adds in a fixed order.
@@ -236,10 +236,10 @@ struct DqStep {
 // tile, rings of 3 K and 1 V tiles.  Warps 0-3 take the keys 0-63 of a tile,
 // warps 4-7 the keys 64-127, one thread per row and half; warps 8, 9, 10 load
 // Q and dO, K, V; warp 11 issues.  The softmax warps compute the next item's D'
-// while this one waits for its sums: a launch of its own for them made 16 heads of
-// 2048 rows x 77 keys take 84 us instead of 74 with gradients, and 40 heads of
-// 32760 rows x 512 keys 1890 instead of 1927; one loader warp for all rows of an
-// item was three times too slow.
+// while this one waits for its sums, which saves a launch: with gradients 16 heads of
+// 2048 rows x 77 keys took 84 us with it and 74 without; 40 heads of 32760 rows x 512
+// keys, where it hid under the others, 1890 with and 1927 without.  One form serves
+// both.  One loader warp for all rows of an item was three times too slow.
 template <typename T, int D>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     cross_dq_kernel(const __grid_constant__ CrossArgs a, const __grid_constant__ CrossMaps m, int items)

@@ -393,8 +393,10 @@ __global__ void __launch_bounds__(kFewThreads, R == 1 ? 3 : R == 2 ? 2 : 1) cros
 // forward, where the products of a second row cost more than those kernels' fixed
 // time (24 heads of 512 keys: 1 row 5.5 us for 10, 4 rows 8.3 for 10; 512 heads of
 // 2048 keys: 4 rows 313 us for 118) or long keys of few heads leave SMs idle
-// (8 heads of 16000 keys: 34 us for 25).  At least 128 keys a CTA, no more CTAs than
-// eight a SM.
+// (8 heads of 16000 keys: 34 us for 25).  The ranks double while a CTA has more than 128
+// keys (so 65 are the fewest) and the sets fewer than eight CTAs a SM (so sixteen are the
+// most).  Not all of those are resident: the bf16 kernel of one row takes 106 registers,
+// two CTAs a SM, so 192 sets of 512 keys on four ranks come in 2.6 rounds.
 int cross_few_ranks(int64_t sets, int64_t rows, int64_t M, bool backward, int sms)
 {
     if (rows < 1 || rows > kFewRows || M < 1) return 0;

@@ -320,7 +320,9 @@ __global__ void __launch_bounds__(512) rope_dw_kernel(const float *part, int par
 // unless that leaves fewer blocks than some six per place on the GPU, whose
 // last ones would run alone (480p, 40 heads: 3.5 blocks a place took 130 us,
 // 7 a place, with the arithmetic below, 115 us); at least eight heads, or a batch where that is
-// needed to fill the GPU at all, as for one token of many heads.
+// needed to fill the GPU at all, as for one token of many heads.  Forward, a place is a
+// quarter of an SM, as the 16-bit kernels fit (52 to 64 registers); of the fp32 ones
+// (80 and 86) an SM holds three or two.
 static int heads_per_block(int64_t token_blocks, int H, int batch, int places)
 {
     int hpb = H;

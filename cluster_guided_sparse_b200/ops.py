@@ -8,6 +8,11 @@ aligned rows, all on one device (which need not be the current one).  A call
 runs on `stream`, by default the current stream of that device; given a
 stream, its outputs and workspace are allocated on it and its inputs are kept
 from reuse until the stream has passed.  Outputs take the inputs' layout.
+
+As with the package's other calls, results carry no autograd graph, whether or not
+inputs require gradients: those come from the _backward functions, which a caller's
+own torch.autograd.Function may wrap.  (The gradient of a plain sum arrives there as
+one expanded element; contiguous() makes the tensor that these calls take.)
 """
 from __future__ import annotations
 

@@ -315,9 +315,11 @@ scope_status scope_kmeans_noalloc(const scope_tensor *x, int32_t dim_off, int32_
 /*                                                                          */
 /* scope_rope (also behind a per-head RMS norm) makes the q and k of a      */
 /* scope_plan call without grid, of scope_cross_attn, or of any attention   */
-/* whose tokens do not fill one raster grid.  scope_cross_attn attends to   */
-/* states of another length; with k, v of the queries' own sequence it is   */
-/* dense self-attention with gradients.  The conventions above hold, and    */
+/* whose tokens do not fill one raster grid.  (The block modes of           */
+/* scope_plan need a grid: they rotate by themselves and take no normed     */
+/* and rotated rows.)  scope_cross_attn attends to states of another        */
+/* length; with k, v of the queries' own sequence it is dense               */
+/* self-attention with gradients.  The conventions above hold, and          */
 /*   - f16 is taken next to bf16 (and f32 by the rotations);                */
 /*   - a tensor without rows (N = 0) is taken; its pointer may be null;     */
 /*   - an output may not overlap an input or another output, except that   */
